@@ -120,6 +120,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "fr_ops_sync_status": (c_int, [c_void_p]),
         "fr_attention_noalloc": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
                                          c_int, c_void_p]),
+        "fr_tree_mask": (c_int, [ctypes.POINTER(ctypes.c_int32), c_int, ctypes.POINTER(ctypes.c_uint32)]),
+        "fr_attention_tree": (c_int, [c_void_p] * 7 + [c_int] * 6 + [c_void_p, ctypes.c_size_t, c_void_p]),
+        "fr_attention_tree_scratch_bytes": (ctypes.c_size_t, [c_int] * 6),
+        "fr_attention_weights": (c_int, [c_void_p] * 7 + [c_int] * 6 + [c_void_p]),
+        "fr_cache_commit": (c_int, [c_void_p] * 8 + [c_int] * 6 + [c_void_p]),
+        "fr_cache_evict": (c_int, [c_void_p] * 9 + [c_int] * 7 + [c_void_p]),
         "fr_prefill": (c_int, [H, c_void_p, c_int, c_int, H, c_void_p]),
         "fr_refresh_prefix_kv": (c_int, [H, c_void_p, c_void_p, ctypes.POINTER(c_int), c_int, c_int, c_uint,
                                          c_void_p]),
@@ -374,6 +380,47 @@ def fr_attention_noalloc(q: int, k: int, v: int, o: int, B: int, Hq: int, Hkv: i
                          stream: int = 0) -> None:
     _check(load_library().fr_attention_noalloc(q, k, v, o, B, Hq, Hkv, H, S_keys, dh, stream),
            "fr_attention_noalloc")
+
+
+FR_TREE_MAX_NODES, FR_CACHE_MAX_SLOTS, FR_EVICT_MAX_SLOTS = 256, 1 << 24, 1 << 19
+
+
+def fr_tree_mask(parents) -> np.ndarray:
+    """Mask words [n][ceil(n/32)] (uint32) of a drafted tree: parents[i] in [-1, i-1]."""
+    p = np.ascontiguousarray(np.asarray(parents, np.int32).ravel())
+    out = np.zeros((p.size, -(-p.size // 32)), np.uint32)
+    _check(load_library().fr_tree_mask(p.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), p.size,
+                                       out.ctypes.data_as(ctypes.POINTER(ctypes.c_uint32))), "fr_tree_mask")
+    return out
+
+
+def fr_attention_tree(q: int, k: int, v: int, lens: int, mask: int, o: int, lse: int, B: int, Hq: int, Hkv: int,
+                      N: int, S_max: int, dh: int, scratch: int = 0, scratch_bytes: int = 0, stream: int = 0) -> None:
+    _check(load_library().fr_attention_tree(q, k, v, lens, mask, o, lse, B, Hq, Hkv, N, S_max, dh, scratch,
+                                            scratch_bytes, stream), "fr_attention_tree")
+
+
+def fr_attention_tree_scratch_bytes(B: int, Hq: int, Hkv: int, N: int, S_max: int, dh: int) -> int:
+    return load_library().fr_attention_tree_scratch_bytes(B, Hq, Hkv, N, S_max, dh)
+
+
+def fr_attention_weights(q: int, k: int, lse: int, lens: int, mask: int, use: int, acc: int, B: int, Hq: int,
+                         Hkv: int, N: int, S_max: int, dh: int, stream: int = 0) -> None:
+    _check(load_library().fr_attention_weights(q, k, lse, lens, mask, use, acc, B, Hq, Hkv, N, S_max, dh, stream),
+           "fr_attention_weights")
+
+
+def fr_cache_commit(k: int, v: int, acc: int, pos: int, lens: int, path: int, npath: int, lens_out: int, B: int,
+                    Hkv: int, N: int, S_max: int, dh: int, dtype: int, stream: int = 0) -> None:
+    _check(load_library().fr_cache_commit(k, v, acc, pos, lens, path, npath, lens_out, B, Hkv, N, S_max, dh, dtype,
+                                          stream), "fr_cache_commit")
+
+
+def fr_cache_evict(k: int, v: int, acc: int, pos: int, lens: int, acc_out: int, pos_out: int, lens_out: int,
+                   src: int, B: int, Hkv: int, S_max: int, dh: int, dtype: int, keep: int, recent: int,
+                   stream: int = 0) -> None:
+    _check(load_library().fr_cache_evict(k, v, acc, pos, lens, acc_out, pos_out, lens_out, src, B, Hkv, S_max, dh,
+                                         dtype, keep, recent, stream), "fr_cache_evict")
 
 
 def fr_rope_tables(n_pos: int, dh: int, theta: float):

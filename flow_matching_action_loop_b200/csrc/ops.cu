@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "cache_ops.h"
 #include "tc_kernels.h"
 
 namespace fr {
@@ -25,7 +26,10 @@ cudaError_t ensure_tc_kernels(int* dev_out) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= MAX_DEVICES) return cudaErrorInvalidDevice;
-  std::call_once(g_init_once[dev], [dev] { g_init_err[dev] = tc::tc_kernels_init(); });
+  std::call_once(g_init_once[dev], [dev] {
+    g_init_err[dev] = tc::tc_kernels_init();
+    if (g_init_err[dev] == cudaSuccess) g_init_err[dev] = tc::cache_ops_init();
+  });
   if (dev_out) *dev_out = dev;
   return g_init_err[dev];
 }
@@ -147,7 +151,7 @@ int fr_ops_sync_status(fr_stream_t stream) {
     set_error("device wait gave up in an op (phase word 0x%08x, block %u)", st[1], st[2]);
     return FR_ERR_TIMEOUT;
   }
-  if (st[0] & ST_BOUNDS) {   // checked builds
+  if (st[0] & ST_BOUNDS) {   // a cache op's sample refused; checked builds: a store's index
     set_error("device bounds check failed in an op (where 0x%08x, index %u)", st[1], st[2]);
     return FR_ERR_DEVICE;
   }

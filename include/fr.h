@@ -452,11 +452,11 @@ int fr_attention(const void* q, const void* k, const void* v, void* o, int B, in
 
 /*
  * fr_ops_sync_status -- synchronise `stream`, then read and clear the status word that the
- * stand-alone ops (fr_attention, fr_attention_noalloc) of the current device latch their
- * device-side failures in.  Returns FR_OK, FR_ERR_TIMEOUT (the message gives the wait's
- * where-code and block) or, in a checked build, FR_ERR_DEVICE (a store's index failed its
- * bounds check: where-code and index).  The word is one per device, shared by every op call
- * on it.
+ * stand-alone ops (fr_attention, fr_attention_noalloc and the cache ops below) of the current
+ * device latch their device-side failures in.  Returns FR_OK, FR_ERR_TIMEOUT (the message gives
+ * the wait's where-code and block) or FR_ERR_DEVICE (where-code and index: a sample whose length
+ * or path a cache op refused or, in a checked build, a store's index that failed its bounds
+ * check).  The word is one per device, shared by every op call on it.
  * Errors: FR_ERR_CUDA.
  */
 int fr_ops_sync_status(fr_stream_t stream);
@@ -489,6 +489,106 @@ size_t fr_attention_scratch_bytes(int B, int Hq, int H, int S_keys, int dh);
  */
 int fr_attention_noalloc(const void* q, const void* k, const void* v, void* o, int B, int Hq, int Hkv, int H,
                          int S_keys, int dh, fr_stream_t stream);
+
+/* ---- kernel library: drafted tokens over a static KV cache ----
+ *
+ * Four ops on one layer's cache, K and V [B][Hkv][S_max][dh] (contiguous; a layer slice of a handle's
+ * named buffers "kv_k" / "kv_v", or any caller buffer).  Sample b holds lens[b] committed tokens in
+ * slots 0..lens[b]-1 and, while drafts are being verified, N drafted tokens in slots lens[b]..
+ * lens[b]+N-1; what later slots hold is never used (it may be stale or not a number).  A step of a
+ * program that decodes drafted tokens is: write the drafts' K/V, fr_attention_tree per layer, decide
+ * what to accept, fr_attention_weights (when the cache is to be trimmed), fr_cache_commit, and now and
+ * then fr_cache_evict.  No counterpart in the pages: they serve a policy that decodes discrete tokens
+ * (a subtask, action tokens) on the backbone's cache after fr_prefill, and histories that outgrow it.
+ *
+ * Common to the four:
+ *   - lens is device int32 [B], so a captured graph follows the sequences' growth.  lens[b] < 0 marks a
+ *     padded sample: nothing of it is read or written (its lens_out is its lens).
+ *   - Kernel-side checks: a sample whose lens[b] (or path, npath) is out of range is skipped, its outputs
+ *     stay as they were, and the fault is latched for fr_ops_sync_status (FR_ERR_DEVICE, the message
+ *     gives the where-code 0xc0.. and the sample).
+ *   - They run on the current device, on `stream`; every pointer must be memory of that device (checked).
+ *     Tensors of 16-byte rows (q, k, v, o) must be 16-byte aligned, the others 4-byte aligned; outputs
+ *     must not overlap inputs.  They allocate nothing and can be captured into graphs (make a first call
+ *     on the device before the capture: it sets kernel attributes); two calls that can overlap in time
+ *     need scratch buffers of their own.  Results do not depend on the launch (no float
+ *     atomics): equal inputs give equal bits.
+ *   - Errors, before any device work: FR_ERR_ARG (NULL or misaligned pointer, memory of another device,
+ *     a size below 1), FR_ERR_SHAPE (N > S_max, keep > S_max, recent > keep, scratch too small),
+ *     FR_ERR_UNSUPPORTED (limits), FR_ERR_CUDA.
+ */
+
+/* Drafted tokens per sample, and tokens of a sample, at most. */
+#define FR_TREE_MAX_NODES 256
+#define FR_CACHE_MAX_SLOTS (1 << 24)
+#define FR_EVICT_MAX_SLOTS (1 << 19)
+
+/* fr_tree_mask -- host utility: the mask words of one sample's tree.  parents[i] in [-1, i-1] is the
+ * drafted token that i continues (-1: the committed tokens).  mask receives [n][ceil(n/32)] words; bit
+ * j % 32 of word j / 32 of row i is set when i sees j: its ancestors and itself.
+ * Errors: FR_ERR_ARG (NULL, a parent out of range), FR_ERR_UNSUPPORTED (n outside [1, FR_TREE_MAX_NODES]). */
+int fr_tree_mask(const int32_t* parents, int n, uint32_t* mask);
+
+/*
+ * fr_attention_tree -- grouped-query attention of N drafted tokens per sample.  Row (query head j, token
+ * i) of sample b attends to every committed slot and to the drafted slots of the tokens it sees, of KV
+ * head floor(j * Hkv / Hq):  o = softmax(q k^T / sqrt(dh)) v,  lse = log sum exp(q k^T / sqrt(dh)).
+ * q: bf16 [B][Hq][N][dh]; k, v: bf16 [B][Hkv][S_max][dh] (keys already rotated); mask: [B][N][ceil(N/32)]
+ * words as fr_tree_mask writes them, any bits (a token need not see itself), or NULL: a sequence, token i
+ * sees drafted tokens 0..i (N = 1 is the decoding of single tokens).  o: bf16 [B][N][Hq*dh] (the layout of
+ * fr_attention); lse: float32 [B][Hq][N], or NULL.  A row that sees no key has o = 0 and lse = -inf.
+ * What a token does not see cannot reach its row, whatever it holds; a drafted value row that holds a NaN
+ * or an infinity makes the whole o row of the tokens that see it NaN.
+ * scratch: fr_attention_tree_scratch_bytes() bytes (NULL when that is 0; 40 MiB cover every size).
+ * Limits: dh in {64, 128, 256}, Hq % Hkv == 0, N <= FR_TREE_MAX_NODES, S_max <= FR_CACHE_MAX_SLOTS,
+ * B <= 4096, Hq <= 1024.
+ */
+int fr_attention_tree(const void* q, const void* k, const void* v, const int32_t* lens, const uint32_t* mask,
+                      void* o, float* lse, int B, int Hq, int Hkv, int N, int S_max, int dh, void* scratch,
+                      size_t scratch_bytes, fr_stream_t stream);
+
+/* Bytes of scratch fr_attention_tree needs for these sizes (0 if none, or if they are out of its limits). */
+size_t fr_attention_tree_scratch_bytes(int B, int Hq, int Hkv, int N, int S_max, int dh);
+
+/*
+ * fr_attention_weights -- the attention weight that each slot received, summed over the rows in use (the
+ * query heads of the KV head's group x the drafted tokens):  w[s] = sum exp(q k_s / sqrt(dh) - lse), over
+ * the rows that see slot s.  acc float32 [B][Hkv][S_max]: committed slots acc[s] += w[s], drafted slots
+ * acc[s] = w[s]; later slots stay as they were.  q, k, lens, mask as fr_attention_tree had them, lse as it
+ * left them (a row of lse = -inf gives nothing); use: [B][ceil(N/32)] words, bit i set when token i
+ * counts (say, was accepted), or NULL: all.  Limits: those of fr_attention_tree.
+ */
+int fr_attention_weights(const void* q, const void* k, const float* lse, const int32_t* lens, const uint32_t* mask,
+                         const uint32_t* use, float* acc, int B, int Hq, int Hkv, int N, int S_max, int dh,
+                         fr_stream_t stream);
+
+/*
+ * fr_cache_commit -- keep the accepted drafted tokens: for i < npath[b], slot lens[b] + i receives slot
+ * lens[b] + path[b][i] (its rows of K and V in every KV head, its acc, its pos), and lens_out[b] =
+ * lens[b] + npath[b].  path: int32 [B][N], each sample's first npath[b] entries ascending in [0, N);
+ * npath: int32 [B], 0 <= npath[b] <= N.  acc float32, pos int32, both [B][Hkv][S_max], either may be NULL.
+ * dtype: FR_DTYPE_BF16 or FR_DTYPE_F32 (the cache's type).  lens_out must not be lens.
+ * Limits: dh <= 512 with rows of a multiple of 16 bytes, N <= FR_TREE_MAX_NODES, S_max <=
+ * FR_CACHE_MAX_SLOTS, B <= 4096, Hkv <= 1024.
+ */
+int fr_cache_commit(void* k, void* v, float* acc, int32_t* pos, const int32_t* lens, const int32_t* path,
+                    const int32_t* npath, int32_t* lens_out, int B, int Hkv, int N, int S_max, int dh, int dtype,
+                    fr_stream_t stream);
+
+/*
+ * fr_cache_evict -- trim each sample to `keep` committed tokens, in each KV head those of largest acc.
+ * Before all others come the tokens of the last `recent` positions: pos > (largest pos of the sample's head)
+ * - recent.  Equal acc: the lowest slot first; a NaN ranks lowest.  Kept tokens below slot `keep` stay; the
+ * others move into the freed slots below `keep`, in ascending order of both (attention over committed
+ * tokens does not depend on their order).  acc_out, pos_out [B][Hkv][S_max] and src int32 [B][Hkv][keep]
+ * receive, per slot j < min(lens[b], keep), the token's acc, pos and old slot; src is -1 after them, and
+ * later entries of acc_out and pos_out stay as they were.  lens_out[b] = min(lens[b], keep).
+ * K and V change in place, rows at or past `keep` stay.  dtype as fr_cache_commit; acc_out, pos_out and
+ * lens_out must not be acc, pos and lens.  Limits: those of fr_cache_commit, S_max <= FR_EVICT_MAX_SLOTS.
+ */
+int fr_cache_evict(void* k, void* v, const float* acc, const int32_t* pos, const int32_t* lens, float* acc_out,
+                   int32_t* pos_out, int32_t* lens_out, int32_t* src, int B, int Hkv, int S_max, int dh, int dtype,
+                   int keep, int recent, fr_stream_t stream);
 
 /* ---- host number-format utilities used by the packer (no GPU needed) ---- */
 

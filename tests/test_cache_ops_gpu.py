@@ -1,0 +1,417 @@
+"""The cache ops (fr_attention_tree, fr_attention_weights, fr_cache_commit, fr_cache_evict) against their
+definitions in 64 bits.
+
+Tolerances, per element.  Products of bf16 values are exact in float32; a dot product of dh terms that is
+summed in float32 is off by at most dh * 2^-24 * sum|q_d k_d| (delta after the scale).  Then
+  lse  delta + (8 + |lse|) * 2^-21: the exponentials' approximation, the running sums, the conversions
+       between base 2 and e, each a few float32 roundings of values up to |lse|;
+  o    2^-8 |o| for the rounding of the output and 2^-8 sum p|v| for that of each p to bf16 (half a bf16
+       step each), and sum p|v| * 2 * (lse's tolerance) for the relative error of each p;
+  acc  w * (lse's tolerance + rows * 2^-24) for the weights' sum, 2^-23 of the result for the last add.
+Slots past the drafted tokens hold NaN in every test, and outputs that must stay as they were a marker.
+"""
+import numpy as np
+import pytest
+
+from tests import _cache as R
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import flow_matching_action_loop_b200 as fr  # noqa: E402
+
+MARK = 7.0
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def seen_of(kind, B, N, rng):
+    """[B][N][N] truth values, or None for the default sequence."""
+    if kind == "chain":
+        return None
+    if kind == "none":
+        return np.zeros((B, N, N), bool)
+    if kind == "random":   # any bits, rows that see nothing among them
+        s = rng.random((B, N, N)) < 0.4
+        s[:, ::3] = False
+        return s
+    out = []
+    for _ in range(B):
+        parents = [int(rng.integers(-1, i)) if i else -1 for i in range(N)]
+        out.append(R.sees(fr.fr_tree_mask(parents), N))
+    return np.stack(out)
+
+
+class Case:
+    def __init__(self, B, Hq, Hkv, dh, N, S_max, lens, kind, seed=0, scale=1.5):
+        rng = np.random.default_rng(seed + 1000 * N + S_max)
+        self.B, self.Hq, self.Hkv, self.dh, self.N, self.S, self.lens = B, Hq, Hkv, dh, N, S_max, lens
+        g = torch.Generator().manual_seed(seed + N + S_max)
+        self.q = (torch.randn(B, Hq, N, dh, generator=g) * scale).bfloat16()
+        self.k = torch.randn(B, Hkv, S_max, dh, generator=g).bfloat16()
+        self.v = torch.randn(B, Hkv, S_max, dh, generator=g).bfloat16()
+        for b, n in enumerate(lens):
+            self.k[b, :, max(n, 0) + N if n >= 0 else 0:] = float("nan")
+            self.v[b, :, max(n, 0) + N if n >= 0 else 0:] = float("nan")
+        seen = seen_of(kind, B, N, rng)
+        self.words = None if seen is None else np.stack([R.words_of(s) for s in seen])
+        self.rng = rng
+
+    def device(self):
+        self.dq, self.dk, self.dv = self.q.cuda(), self.k.cuda(), self.v.cuda()
+        self.dlens = torch.tensor(self.lens, dtype=torch.int32, device="cuda")
+        self.dwords = None if self.words is None else torch.from_numpy(self.words.view(np.int32)).cuda()
+        self.o = torch.full((self.B, self.N, self.Hq * self.dh), MARK, dtype=torch.bfloat16, device="cuda")
+        self.lse = torch.full((self.B, self.Hq, self.N), MARK, device="cuda")
+        self.nscratch = fr.fr_attention_tree_scratch_bytes(self.B, self.Hq, self.Hkv, self.N, self.S, self.dh)
+        # a fresh workspace holds anything
+        self.scratch = torch.full((max(self.nscratch, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+        return self
+
+    def run(self):
+        fr.fr_attention_tree(ptr(self.dq), ptr(self.dk), ptr(self.dv), ptr(self.dlens), ptr(self.dwords), ptr(self.o),
+                             ptr(self.lse), self.B, self.Hq, self.Hkv, self.N, self.S, self.dh, ptr(self.scratch),
+                             self.nscratch, stream())
+
+    def oracle(self):
+        return R.attend(self.q.double().numpy(), self.k.double().numpy(), self.v.double().numpy(), self.lens, self.words)
+
+
+def check(c, o, lse, oracle=None):
+    want, pv, wlse, size = oracle or c.oracle()
+    got = o.float().cpu().numpy().reshape(want.shape).astype(np.float64)
+    glse = lse.cpu().numpy().astype(np.float64)
+    for b, n in enumerate(c.lens):
+        if n < 0:
+            assert np.all(got[b] == MARK) and np.all(glse[b] == MARK)
+            continue
+        empty = np.isinf(wlse[b])
+        assert np.array_equal(glse[b] == -np.inf, empty)
+        fin = np.where(empty, 0.0, wlse[b])
+        tl = c.dh * 2.0 ** -24 * size[b] + (8 + np.abs(fin)) * 2.0 ** -21
+        d = np.abs(np.where(empty, 0.0, glse[b]) - fin)
+        assert np.all(d <= tl), (b, d.max(), tl.min())
+        tol = 2.0 ** -8 * (np.abs(want[b]) + pv[b]) + pv[b] * 2 * tl.T[:, :, None] + 1e-30
+        d = np.abs(got[b] - want[b])
+        assert np.all(d <= tol), (b, float(d.max()), np.unravel_index(np.argmax(d - tol), d.shape))
+
+
+ATTEND = [
+    # B, Hq, Hkv, dh, N, S_max, lens, mask
+    (1, 1, 1, 64, 1, 1, [0], "chain"),                        # one token that sees itself alone
+    (1, 8, 1, 256, 1, 866, [816], "chain"),                   # the backbone's heads over one prefix
+    (2, 4, 2, 128, 1, 2, [0, 1], "none"),                     # nothing to see; one committed slot
+    (3, 2, 1, 64, 5, 140, [127, -1, 0], "tree"),              # a padded sample between others
+    (4, 16, 2, 128, 24, 160, [128, 129, 127, 136], "tree"),   # tiles that end at, before and after the drafts
+    (2, 8, 1, 256, 33, 300, [200, 31], "random"),             # rows that see no drafted token
+    (2, 8, 1, 256, 17, 17, [0, 0], "random"),                 # rows that see nothing at all
+    (1, 3, 3, 64, 256, 700, [444], "tree"),                   # as many drafted tokens as there may be
+    (1, 4, 1, 64, 256, 513, [257], "chain"),                  # eight row tiles, a sequence
+    (2, 7, 1, 128, 19, 515, [496, 300], "tree"),              # a group of seven, 133 rows
+    (5, 12, 4, 64, 3, 130, [1, 2, 60, 127, -5], "tree"),
+    (9, 2, 2, 128, 2, 1000, [0, 998, 5, 640, 127, 128, 384, 900, 1], "chain"),   # ragged
+    (1, 2, 1, 64, 2, 40000, [39998], "chain"),                # long
+    (1, 8, 1, 256, 16, 5000, [4800], "tree"),                 # 128 rows, many tiles
+    (40, 8, 8, 64, 1, 200, [150 + i % 40 for i in range(40)], "chain"),          # more units than SMs
+    (33, 5, 5, 128, 4, 300, [(37 * i) % 297 for i in range(33)], "tree"),
+]
+
+
+@pytest.mark.parametrize("spec", ATTEND, ids=lambda s: "-".join(map(str, s[:6])) + "-" + s[7])
+def test_tree_attention(spec):
+    c = Case(*spec).device()
+    c.run()
+    first = (c.o.clone(), c.lse.clone())
+    check(c, *first)
+    c.run()   # the workspace as the first call left it: the same bits
+    assert torch.equal(c.o, first[0]) and torch.equal(c.lse, first[1])
+    assert fr.fr_ops_sync_status(stream()) == 0
+
+
+@pytest.mark.parametrize("dh", [64, 128, 256])
+def test_tree_attention_large_scores(dh):
+    """Scores of both signs up to hundreds, growing along the cache: the running maximum moves in many tiles."""
+    c = Case(1, 4, 1, dh, 9, 900, [800], "tree", seed=3, scale=6.0)
+    c.k[0, 0, :809] *= torch.linspace(0.05, 4.0, 809)[:, None].to(torch.bfloat16)
+    c.device().run()
+    check(c, c.o, c.lse)
+
+
+def test_tree_attention_hidden_values_do_not_leak():
+    """A drafted token with NaN or infinite K and V reaches the rows that see it and no others."""
+    c = Case(1, 8, 1, 128, 40, 400, [301], "chain")
+    hidden = [3, 17, 39]
+    seen = np.tril(np.ones((40, 40), bool))
+    seen[:, hidden] = False
+    seen[hidden, hidden] = True
+    c.words = R.words_of(seen)[None]
+    oracle = c.oracle()
+    c.k[0, 0, 301 + 3], c.v[0, 0, 301 + 3] = float("nan"), float("nan")
+    c.k[0, 0, 301 + 17], c.v[0, 0, 301 + 17] = float("inf"), float("-inf")
+    c.v[0, 0, 301 + 39, 5] = float("inf")
+    c.device().run()
+    got = c.o.view(40, 8, 128).float()
+    for i in hidden:
+        assert torch.isnan(got[i]).all()
+        c.o.view(40, 8, 128)[i] = torch.from_numpy(oracle[0][0, i]).cuda().bfloat16()
+        c.lse[0, :, i] = torch.from_numpy(oracle[2][0, :, i]).cuda().float()
+    check(c, c.o, c.lse, oracle)
+
+
+def test_tree_attention_refuses_bad_lengths_on_the_device():
+    c = Case(4, 4, 2, 64, 3, 100, [50, 97, 20, 4], "tree").device()
+    c.dlens[0], c.dlens[2] = 98, 2 ** 31 - 1      # lens + N past the cache
+    c.lens = [-1, 97, -1, 4]                      # the oracle's view: skipped samples
+    c.run()
+    check(c, c.o, c.lse)
+    with pytest.raises(fr.FrError) as e:
+        fr.fr_ops_sync_status(stream())
+    assert e.value.code == fr.FR_ERR_DEVICE and "c001" in str(e.value)
+    assert fr.fr_ops_sync_status(stream()) == 0
+
+
+def test_tree_attention_without_lse_and_in_a_graph():
+    """lse may be NULL; a captured call follows lens and mask as they change between replays."""
+    c = Case(3, 8, 2, 128, 6, 700, [600, 30, -1], "tree").device()
+    c.run()
+    o = c.o.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        fr.fr_attention_tree(ptr(c.dq), ptr(c.dk), ptr(c.dv), ptr(c.dlens), ptr(c.dwords), ptr(c.o), 0, c.B, c.Hq, c.Hkv,
+                             c.N, c.S, c.dh, ptr(c.scratch), c.nscratch, torch.cuda.current_stream().cuda_stream)
+    c.o.fill_(MARK)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(c.o, o)
+    c.lens = [100, -1, 17]
+    c.dlens.copy_(torch.tensor(c.lens, dtype=torch.int32))
+    c.words[:] = c.words[::-1].copy()
+    c.dwords.copy_(torch.from_numpy(c.words.view(np.int32)))
+    # the third sample's cache was padding; give it rows
+    c.k[2, :, :23], c.v[2, :, :23] = c.k[0, :, :23], c.v[0, :, :23]
+    c.dk.copy_(c.k), c.dv.copy_(c.v)
+    c.o.fill_(MARK)
+    graph.replay()
+    want = c.o.clone()
+    c.o.fill_(MARK), c.lse.fill_(MARK)
+    c.run()
+    assert torch.equal(c.o, want)
+    check(c, c.o, c.lse)
+
+
+def test_tree_attention_on_two_streams_with_their_own_workspaces():
+    a, b = Case(2, 8, 1, 256, 9, 3000, [2500, 2900], "tree").device(), Case(2, 8, 1, 256, 9, 3000, [100, 1700], "tree", seed=9).device()
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for c, st in zip((a, b), s):
+            with torch.cuda.stream(st):
+                c.run()
+    torch.cuda.synchronize()
+    check(a, a.o, a.lse)
+    check(b, b.o, b.lse)
+
+
+WEIGH = [s for s in ATTEND if s[5] <= 5000]
+
+
+@pytest.mark.parametrize("spec", WEIGH, ids=lambda s: "-".join(map(str, s[:6])) + "-" + s[7])
+@pytest.mark.parametrize("some", [False, True])
+def test_attention_weights(spec, some):
+    c = Case(*spec).device()
+    N = c.N
+    use = None
+    if some:
+        use = np.zeros((c.B, -(-N // 32)), np.uint32)
+        for b in range(c.B):
+            for i in range(N):
+                if c.rng.random() < 0.5:
+                    use[b, i // 32] |= np.uint32(1 << (i % 32))
+    _, _, lse, size = c.oracle()
+    lse32 = torch.from_numpy(lse).float()
+    acc = torch.rand(c.B, c.Hkv, c.S, generator=torch.Generator().manual_seed(5))
+    d_acc, d_lse = acc.cuda(), lse32.cuda()
+    d_use = None if use is None else torch.from_numpy(use.view(np.int32)).cuda()
+
+    def call():
+        fr.fr_attention_weights(ptr(c.dq), ptr(c.dk), ptr(d_lse), ptr(c.dlens), ptr(c.dwords), ptr(d_use), ptr(d_acc),
+                                c.B, c.Hq, c.Hkv, N, c.S, c.dh, stream())
+    call()
+    want, w = R.weigh(c.q.double().numpy(), c.k.double().numpy(), lse32.double().numpy(), c.lens, c.words, use, acc.numpy())
+    got = d_acc.cpu().numpy().astype(np.float64)
+    rows = c.Hq // c.Hkv * N
+    fin = np.where(np.isinf(lse), 0.0, np.abs(lse))
+    tl = c.dh * 2.0 ** -24 * size.max() + (8 + fin.max()) * 2.0 ** -21
+    for b, n in enumerate(c.lens):
+        used = n + N if n >= 0 else 0
+        assert np.array_equal(got[b, :, used:], acc[b, :, used:].double().numpy())
+        d = np.abs(got[b, :, :used] - want[b, :, :used])
+        assert np.all(d <= w[b, :, :used] * (tl + rows * 2.0 ** -24) + 2.0 ** -23 * want[b, :, :used] + 1e-37), d.max()
+    once = d_acc.clone()
+    d_acc.copy_(acc)
+    call()
+    assert torch.equal(d_acc, once)   # the same bits
+    assert fr.fr_ops_sync_status(stream()) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,Hkv,dh,N,S,lens", [
+    (1, 1, 256, 24, 866, [816]),
+    (3, 2, 64, 1, 9, [0, 8, -1]),
+    (4, 3, 128, 63, 200, [137, 0, 100, 50]),
+    (2, 1, 512, 256, 600, [344, 1]),
+    (2, 2, 8, 256, 300, [44, 0]),
+    (1, 1, 24, 40, 41, [1]),
+])
+@pytest.mark.parametrize("optional", [True, False])
+def test_commit(B, Hkv, dh, N, S, lens, dtype, optional):
+    rng = np.random.default_rng(N + S)
+    g = torch.Generator().manual_seed(N)
+    k, v = torch.randn(B, Hkv, S, dh, generator=g).to(dtype), torch.randn(B, Hkv, S, dh, generator=g).to(dtype)
+    acc, pos = torch.rand(B, Hkv, S, generator=g), torch.randint(0, 1 << 30, (B, Hkv, S), generator=g, dtype=torch.int32)
+    for trial in range(4):
+        npath = [[0, N, int(rng.integers(0, N + 1)), 1][(trial + b) % 4] for b in range(B)]
+        path = np.full((B, N), -9, np.int32)   # entries past npath are not looked at
+        for b in range(B):
+            path[b, :npath[b]] = np.sort(rng.permutation(N)[:npath[b]])
+        t = [x.clone() for x in (k, v, acc, pos)]
+        out = lens[:]
+        for b, n in enumerate(lens):
+            if n < 0:
+                continue
+            at = n + path[b, :npath[b]].astype(np.int64)
+            for x in t if optional else t[:2]:
+                x[b, :, n:n + npath[b]] = x[b][:, torch.from_numpy(at)]
+            out[b] = n + npath[b]
+        dev = [x.cuda() for x in (k, v, acc, pos)]
+        d_lens = torch.tensor(lens, dtype=torch.int32).cuda()
+        d_path, d_np = torch.from_numpy(path).cuda(), torch.tensor(npath, dtype=torch.int32).cuda()
+        d_out = torch.full((B,), 99, dtype=torch.int32, device="cuda")
+        fr.fr_cache_commit(ptr(dev[0]), ptr(dev[1]), ptr(dev[2]) if optional else 0, ptr(dev[3]) if optional else 0,
+                           ptr(d_lens), ptr(d_path), ptr(d_np), ptr(d_out), B, Hkv, N, S, dh,
+                           fr.FR_DTYPE_F32 if dtype == torch.float32 else fr.FR_DTYPE_BF16, stream())
+        for x, y in zip(dev, t):
+            assert torch.equal(x.cpu(), y)
+        assert d_out.tolist() == out
+        assert fr.fr_ops_sync_status(stream()) == 0
+
+
+def test_commit_refuses_bad_paths_on_the_device():
+    B, Hkv, N, S, dh = 6, 2, 4, 50, 64
+    k = torch.randn(B, Hkv, S, dh).cuda()
+    v, k0 = k.clone() + 1, k.clone()
+    lens = torch.tensor([10, 10, 10, 47, 10, 10], dtype=torch.int32).cuda()
+    path = torch.tensor([[0, 2, 1, 3], [0, 1, 2, 4], [1, 1, 2, 3], [0, 1, 2, 3], [-1, 0, 1, 2], [1, 3, 0, 0]], dtype=torch.int32).cuda()
+    npath = torch.tensor([3, 4, 2, 1, 1, 2], dtype=torch.int32).cuda()
+    out = torch.zeros(B, dtype=torch.int32).cuda()
+    fr.fr_cache_commit(ptr(k), ptr(v), 0, 0, ptr(lens), ptr(path), ptr(npath), ptr(out), B, Hkv, N, S, dh, fr.FR_DTYPE_F32, stream())
+    assert out.tolist() == [10, 10, 10, 47, 10, 12]
+    want = k0.clone()
+    want[5, :, 10:12] = k0[5][:, [11, 13]]
+    assert torch.equal(k, want) and torch.equal(v, want + 1)
+    with pytest.raises(fr.FrError) as e:
+        fr.fr_ops_sync_status(stream())
+    assert e.value.code == fr.FR_ERR_DEVICE
+    npath.copy_(torch.tensor([5, -1, 0, 0, 0, 0], dtype=torch.int32))
+    lens[3] = -1
+    fr.fr_cache_commit(ptr(k), ptr(v), 0, 0, ptr(lens), ptr(path), ptr(npath), ptr(out), B, Hkv, N, S, dh, fr.FR_DTYPE_F32, stream())
+    assert out.tolist() == [10, 10, 10, -1, 10, 10] and torch.equal(k, want)
+    with pytest.raises(fr.FrError) as e:
+        fr.fr_ops_sync_status(stream())
+    assert "c002" in str(e.value)
+
+
+EVICT = [
+    # B, Hkv, dh, S_max, lens, keep, recent, weights, dtype
+    (1, 1, 256, 866, [866], 512, 50, "spread", "bf16"),
+    (1, 1, 8, 1, [1], 1, 0, "spread", "bf16"),
+    (3, 2, 64, 40, [0, 40, -1], 1, 1, "spread", "f32"),
+    (4, 2, 64, 300, [299, 128, 129, 300], 128, 0, "ties", "bf16"),
+    (4, 2, 64, 300, [299, 128, 129, 300], 128, 128, "spread", "f32"),     # every kept slot protected
+    (2, 3, 128, 3000, [2999, 2050], 2049, 7, "few", "bf16"),
+    (2, 1, 64, 9000, [9000, 6001], 600, 64, "ties", "bf16"),
+    (1, 2, 64, 40001, [40001], 39999, 1000, "spread", "bf16"),
+    (2, 1, 16, 70000, [70000, 69999], 10, 3, "odd", "f32"),
+    (1, 1, 8, 524288, [524288], 262145, 100, "spread", "bf16"),           # as many slots as there may be
+    (30, 4, 64, 500, [499 - 7 * i for i in range(30)], 333, 33, "few", "f32"),
+    (2, 2, 512, 260, [250, 100], 99, 0, "equal", "f32"),
+]
+
+
+@pytest.mark.parametrize("B,Hkv,dh,S,lens,keep,recent,weights,dt", EVICT)
+def test_evict(B, Hkv, dh, S, lens, keep, recent, weights, dt):
+    rng = np.random.default_rng(S + keep)
+    dtype = torch.float32 if dt == "f32" else torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(S)
+    k = torch.randn(B, Hkv, S, dh, generator=g, device="cuda").to(dtype)
+    v = torch.randn(B, Hkv, S, dh, generator=g, device="cuda").to(dtype)
+    if weights == "spread":
+        acc = np.exp(rng.standard_normal((B, Hkv, S)) * 3)
+    elif weights == "ties":
+        acc = rng.integers(0, 4, (B, Hkv, S)).astype(np.float64)
+    elif weights == "few":
+        acc = np.where(rng.random((B, Hkv, S)) < 0.02, 5.0, rng.random((B, Hkv, S)) * 2.0 ** -140)
+    elif weights == "equal":
+        acc = np.zeros((B, Hkv, S))
+    else:   # signs, zeros of both signs, infinities, NaN
+        acc = rng.choice([0.0, -0.0, -1.5, 2.0, np.inf, -np.inf, np.nan, 1e-45, -1e-45], (B, Hkv, S))
+    acc = acc.astype(np.float32)
+    pos = np.stack([[rng.permutation(S).astype(np.int32) - (5 if weights == "odd" else 0) for _ in range(Hkv)] for _ in range(B)])
+    d_acc, d_pos = torch.from_numpy(acc).cuda(), torch.from_numpy(pos).cuda()
+    d_lens = torch.tensor(lens, dtype=torch.int32).cuda()
+    acc_out, pos_out = torch.full_like(d_acc, MARK), torch.full_like(d_pos, 7)
+    src, lens_out = torch.full((B, Hkv, keep), 77, dtype=torch.int32, device="cuda"), torch.full((B,), 99, dtype=torch.int32, device="cuda")
+    k1, v1 = k.clone(), v.clone()
+    fr.fr_cache_evict(ptr(k1), ptr(v1), ptr(d_acc), ptr(d_pos), ptr(d_lens), ptr(acc_out), ptr(pos_out), ptr(lens_out),
+                      ptr(src), B, Hkv, S, dh, fr.FR_DTYPE_F32 if dt == "f32" else fr.FR_DTYPE_BF16, keep, recent, stream())
+    assert fr.fr_ops_sync_status(stream()) == 0
+    assert lens_out.tolist() == [min(n, keep) for n in lens]
+    wk, wv = k.clone(), v.clone()
+    wacc, wpos, wsrc = np.full_like(acc, MARK), np.full_like(pos, 7), np.full((B, Hkv, keep), 77, np.int32)
+    for b, n in enumerate(lens):
+        for h in range(Hkv if n >= 0 else 0):
+            at = R.evict_one(acc[b, h, :n], pos[b, h, :n], keep, recent)
+            m = len(at)
+            wsrc[b, h, :m], wsrc[b, h, m:] = at, -1
+            wacc[b, h, :m], wpos[b, h, :m] = acc[b, h][at], pos[b, h][at]
+            t = torch.from_numpy(at).cuda()
+            wk[b, h, :m], wv[b, h, :m] = k[b, h][t], v[b, h][t]
+    assert np.array_equal(src.cpu().numpy(), wsrc)
+    assert np.array_equal(acc_out.cpu().numpy(), wacc, equal_nan=True) and np.array_equal(pos_out.cpu().numpy(), wpos)
+    assert torch.equal(k1, wk) and torch.equal(v1, wv)
+    assert torch.equal(d_acc.cpu(), torch.from_numpy(acc)) or weights == "odd"
+
+
+def test_evict_refuses_bad_lengths_on_the_device():
+    B, Hkv, S, dh, keep = 3, 2, 64, 64, 8
+    k = torch.randn(B, Hkv, S, dh).cuda()
+    k0, v = k.clone(), k.clone()
+    acc, pos = torch.rand(B, Hkv, S).cuda(), torch.arange(S, dtype=torch.int32).expand(B, Hkv, S).contiguous().cuda()
+    lens = torch.tensor([65, 8, 2 ** 30], dtype=torch.int32).cuda()
+    outs = [torch.full_like(acc, MARK), torch.full_like(pos, 7), torch.zeros_like(lens), torch.full((B, Hkv, keep), 77, dtype=torch.int32).cuda()]
+    fr.fr_cache_evict(ptr(k), ptr(v), ptr(acc), ptr(pos), ptr(lens), *[ptr(t) for t in outs], B, Hkv, S, dh, fr.FR_DTYPE_F32, keep, 2, stream())
+    assert torch.equal(k, k0) and outs[2].tolist() == [65, 8, 2 ** 30]
+    assert (outs[0][[0, 2]] == MARK).all() and (outs[3][[0, 2]] == 77).all() and outs[3][1, 0].tolist() == list(range(8))
+    with pytest.raises(fr.FrError) as e:
+        fr.fr_ops_sync_status(stream())
+    assert e.value.code == fr.FR_ERR_DEVICE and "c001" in str(e.value)
+
+
+def test_pointers_of_the_host_are_refused():
+    t = torch.zeros(4096, dtype=torch.bfloat16)
+    d = torch.zeros(4096, dtype=torch.bfloat16, device="cuda")
+    n = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for q, k, lens in ((t, d, n), (d, t, n), (d, d, torch.zeros(4, dtype=torch.int32))):
+        with pytest.raises(fr.FrError) as e:
+            fr.fr_attention_tree(ptr(q), ptr(k), ptr(d), ptr(lens), 0, ptr(d), 0, 1, 1, 1, 1, 8, 64, 0, 0, stream())
+        assert e.value.code == fr.FR_ERR_ARG and "current device" in str(e.value)
