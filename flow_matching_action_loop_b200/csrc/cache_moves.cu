@@ -3,22 +3,14 @@
 #include <algorithm>
 #include <cooperative_groups.h>
 
-#include "cache_ops.h"
 #include "fr.h"
-#include "tc_device.h"
+#include "tree_device.h"
 
 namespace fr {
 namespace tc {
 namespace {
 
 namespace cg = cooperative_groups;
-
-__device__ __forceinline__ void report_sample(unsigned* status, uint32_t where, int sample) {
-  if (!(atomicOr(status, ST_BOUNDS_BIT) & ST_BOUNDS_BIT)) {   // the first refused sample reports
-    atomicExch(status + 1, where);
-    atomicExch(status + 2, static_cast<unsigned>(sample));
-  }
-}
 
 // ------------------------------------------------------------------ commit
 // One CTA per (K or V, KV head, sample).  path ascends, so row i moves down (path[i] >= i) and no later

@@ -3,8 +3,10 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 namespace fr {
 
@@ -30,6 +32,8 @@ struct TreeArgs {
   unsigned* status;
   int B, Hq, Hkv, N, W, S_max, dh;
   float scale;                 // 1/sqrt(dh)
+  int ctas;                    // attention: CTAs that share the tiles
+  CUtensorMap tm_q, tm_k, tm_v;   // written by the launchers
 };
 
 struct MoveArgs {
@@ -50,6 +54,7 @@ struct MoveArgs {
   int B, Hkv, N, S_max, row_bytes, keep, recent;
 };
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // tc_kernels.cu
 cudaError_t cache_ops_init();   // kernel attributes, once per device
 size_t tree_scratch_bytes(int B, int Hq, int Hkv, int N, int S_max, int dh);
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);

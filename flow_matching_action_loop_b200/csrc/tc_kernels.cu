@@ -2050,8 +2050,6 @@ cudaError_t launch_gemm_tc(const GemmArgs& a, int n_tiles, cudaStream_t s, bool 
                    pdl, a.S, args);
 }
 
-namespace {
-
 // cuTensorMapEncodeTiled from the driver, found once through the runtime (no link-time dependency).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -2065,6 +2063,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
+
+namespace {
 
 // Tensor map of K or V ([planes][keys][dh] bf16, planes plane_bytes apart), 128-byte swizzle; keys past
 // `keys` read as zeros.  one_box: the 4-D view (64 features, keys, dh/64 feature blocks, planes) with

@@ -1,132 +1,671 @@
-// Attention of drafted tokens over a static KV cache, and the weights its slots received.
+// Attention of drafted tokens over a static KV cache (fr_attention_tree).
+//
+// The rows of a unit (sample, KV head, row tile) are up to 128 of the (query head, token) pairs that read
+// the KV head, so that its K and V are read once for the whole group; its keys come in tiles of 128 slots.
+// All units' tiles form one line that the CTAs (one per SM) cut into equal ranges, whatever the samples'
+// lengths: a CTA runs the segments of units that lie in its range one after the other.  A segment that is
+// its whole unit writes o and lse; one that is part of a unit writes its rows (O, reference, sum) to the
+// scratch, and k_tree_merge, chained behind, joins them.
+//
+// Inside a CTA, per tile t:
+//   copy warp     K(t+1), V(t) by tensor map (128-byte swizzle) into a ring of shared-memory slots
+//   MMA warp      S(t+1) = Q K(t+1)^T, then O += P(t) V(t): tcgen05, fp32 in tensor memory; P is the A
+//                 operand from tensor memory, in the columns of the scores it came from
+//   softmax warps (8) two threads per row, 64 slots each: running maximum and sum in fp32, P = 2^(s - ref)
+// so the tensor core works on S(t+1) and P(t-1) V(t-1) while the softmax of tile t runs.  The reference
+// of a row's exponentials moves only when its maximum has grown by more than 2^8 (P stays below 2^8, O and
+// the sum keep one reference, O / sum is unchanged): O is rescaled rarely.
+// P is rounded to bf16, the tensor core's operand type: half a bf16 step per weight, as much as the
+// rounding of o itself.
 #include <algorithm>
+#include <type_traits>
 
-#include "cache_ops.h"
 #include "fr.h"
-#include "tc_device.h"
+#include "tree_device.h"
 
 namespace fr {
 namespace tc {
 namespace {
 
-__device__ __forceinline__ void report_sample(unsigned* status, uint32_t where, int sample) {
-  if (!(atomicOr(status, ST_BOUNDS_BIT) & ST_BOUNDS_BIT)) {   // the first refused sample reports
-    atomicExch(status + 1, where);
-    atomicExch(status + 2, static_cast<unsigned>(sample));
+using namespace fr::sm100;
+
+constexpr int TA_SOFTMAX = 256;                // softmax threads
+constexpr int TA_THREADS = TA_SOFTMAX + 64;    // + the copy warp and the MMA warp
+constexpr int TA_CTAS = 148;                   // at most: the scratch holds two segments' rows for each
+constexpr float TA_RESCALE = 8.f;
+
+// Shared memory: QB query tiles, then NS ring slots of `piece` bytes.  At dh = 256 a K tile comes as two
+// pieces of 128 features, a V tile as two of 64 slots, so that the ring has five slots instead of two.
+template <int DH>
+struct TreeGeom {
+  static constexpr int pieces = DH == 256 ? 2 : 1;              // per K or V tile
+  static constexpr int piece = TREE_KEYS * DH * 2 / pieces;     // bytes
+  static constexpr int QB = DH == 256 ? 1 : 2;
+  static constexpr int NS = DH == 64 ? 10 : 5;
+  static constexpr int q_bytes = 128 * DH * 2;
+  static constexpr int smem = QB * q_bytes + NS * piece;
+  static constexpr int v_keys = TREE_KEYS / pieces;             // slots per V piece
+  static constexpr int k_blocks = DH / 64 / pieces;             // feature blocks per K piece
+};
+
+// The line of tiles: sample b's units (KV head major, row tile minor), tiles minor.
+struct TileRange {
+  long long t0, t1, cum;   // this CTA's tiles; first tile of sample b
+  int b;                   // sample of t0
+};
+
+struct TileIter {
+  long long t, t1, cum;
+  int b, nb, U;
+  // segment
+  int len, hk, rt, tile0, tile1, first;
+  __device__ __forceinline__ void start(const TreeArgs& a, const TileRange& r, int U_) {
+    t = r.t0;
+    t1 = r.t1;
+    cum = r.cum;
+    b = r.b;
+    U = U_;
+    first = 1;
+    nb = t < t1 ? sample_tiles(a, b) : 0;
   }
-}
-
-// Whether token n sees slot s of sample b (len committed tokens).
-__device__ __forceinline__ bool sees(const TreeArgs& a, int b, int n, int len, int s) {
-  if (s < len) return true;
-  const int j = s - len;
-  if (j >= a.N) return false;
-  if (!a.mask) return j <= n;
-  return (a.mask[(static_cast<size_t>(b) * a.N + n) * a.W + (j >> 5)] >> (j & 31)) & 1u;
-}
-
-__device__ __forceinline__ float dot_row(const float* q, const __nv_bfloat16* k, int dh) {
-  float s = 0.f;
-  for (int d = 0; d < dh; ++d) s = fmaf(q[d], __bfloat162float(k[d]), s);
-  return s;
-}
-
-// One CTA per row (token, head, sample), 128 keys at a time.
-__global__ void __launch_bounds__(128) k_tree_rows(const __grid_constant__ TreeArgs a) {
-  __shared__ float q[256], p[128], red[4];
-  __shared__ bool vis[128];
-  __shared__ int poison;   // a drafted value row that this token sees is not finite
-  const int n = blockIdx.x, hq = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int len = a.lens[b];
-  if (len < 0 || len > a.S_max - a.N) {
-    if (len > 0 && n == 0 && hq == 0 && tid == 0) report_sample(a.status, CACHE_BAD_LEN, b);
-    return;
-  }
-  const size_t row = (static_cast<size_t>(b) * a.Hq + hq) * a.N + n;
-  const size_t kv0 = (static_cast<size_t>(b) * a.Hkv + hq / (a.Hq / a.Hkv)) * a.S_max * a.dh;
-  for (int d = tid; d < a.dh; d += 128) q[d] = __bfloat162float(a.q[row * a.dh + d]) * a.scale;
-  if (tid == 0) poison = 0;
-  float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
-  const int S = len + a.N;
-  for (int s0 = 0; s0 < S; s0 += 128) {
-    __syncthreads();
-    const bool v = s0 + tid < S && sees(a, b, n, len, s0 + tid);
-    const float sc = v ? dot_row(q, a.k + kv0 + static_cast<size_t>(s0 + tid) * a.dh, a.dh) : -INFINITY;
-    float mx = sc;
-    for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    const float mn = fmaxf(fmaxf(m, fmaxf(red[0], red[1])), fmaxf(red[2], red[3]));
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    vis[tid] = v;
-    p[tid] = v ? expf(sc - ref) : 0.f;
-    const float corr = expf(m - ref);
-    __syncthreads();
-    l *= corr;
-    o[0] *= corr;
-    o[1] *= corr;
-    for (int j = 0; j < min(128, S - s0); ++j) {
-      if (!vis[j]) continue;
-      l += p[j];
-      for (int e = 0; e < 2; ++e)
-        if (tid + 128 * e < a.dh) {
-          const float v = __bfloat162float(a.v[kv0 + static_cast<size_t>(s0 + j) * a.dh + tid + 128 * e]);
-          if (s0 + j >= len && !isfinite(v)) poison = 1;
-          o[e] = fmaf(p[j], v, o[e]);
-        }
+  __device__ __forceinline__ bool next(const TreeArgs& a, int RT) {
+    if (t >= t1) return false;
+    while (t - cum >= static_cast<long long>(U) * nb) {
+      cum += static_cast<long long>(U) * nb;
+      nb = sample_tiles(a, ++b);
     }
-    m = mn;
+    const int rel = static_cast<int>(t - cum), u = rel / nb;
+    len = a.lens[b];
+    hk = u / RT;
+    rt = u - hk * RT;
+    tile0 = rel - u * nb;
+    tile1 = static_cast<int>(min(static_cast<long long>(nb), tile0 + (t1 - t)));
+    t += tile1 - tile0;
+    return true;
+  }
+};
+
+// One warp: the number of tiles, the tiles before sample b_of (or, b_of < 0, the sample that holds tile
+// `at` and the tiles before it).
+__device__ __forceinline__ long long tiles_before(const TreeArgs& a, int U, int b_end, unsigned* status) {
+  const int lane = threadIdx.x & 31;
+  long long sum = 0;
+  for (int b0 = 0; b0 < b_end; b0 += 32) {
+    const int b = b0 + lane;
+    int n = 0;
+    if (b < b_end) {
+      n = sample_tiles(a, b);
+      if (status && n == 0 && a.lens[b] >= 0) report_sample(status, CACHE_BAD_LEN, b);
+    }
+    sum += n;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum * U;
+}
+
+__device__ __forceinline__ void find_tile(const TreeArgs& a, int U, long long at, int& b_at, long long& cum_at) {
+  const int lane = threadIdx.x & 31;
+  long long cum = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const long long n = b0 + lane < a.B ? static_cast<long long>(sample_tiles(a, b0 + lane)) * U : 0;
+    long long incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, cum + incl > at);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      b_at = b0 + l;
+      cum_at = cum + __shfl_sync(0xffffffffu, incl - n, l);
+      return;
+    }
+    cum += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+__device__ __forceinline__ void pair_barrier(int w) { asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory"); }
+__device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
+
+template <int DH>
+__global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_constant__ TreeArgs a) {
+  using G = TreeGeom<DH>;
+  extern __shared__ __align__(1024) uint8_t dsm[];
+  __shared__ uint64_t full[G::NS], empty[G::NS], q_full[2], q_empty[2], bar_s[2], bar_o[2], bar_p[2], fin_bar;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  __shared__ TileRange range;
+  __shared__ float mx_sh[2][2][128];       // [tile parity][half][row]; a segment's sums at its end
+  __shared__ uint32_t bad[3][4];           // drafted value rows of a tile that are not finite
+  constexpr uint32_t IDESC_S = idesc_f32acc(FMT_BF16, 128, TREE_KEYS);
+  constexpr uint32_t IDESC_O = idesc_f32acc(FMT_BF16, 128, DH) | IDESC_B_MN_MAJOR;
+  constexpr int OLD = DH + 4;              // floats per partial row: O, reference, sum, NaN if spoilt
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int g = a.Hq / a.Hkv, R = g * a.N, RT = (R + 127) >> 7, U = a.Hkv * RT;
+
+  if (tid == 0) {
+    for (int i = 0; i < G::NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_o[i], 1);
+      mbar_init(&bar_p[i], TA_SOFTMAX / 32);
+    }
+    mbar_init(&fin_bar, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (tid < 12) bad[tid >> 2][tid & 3] = 0;
+  if (warp == 0) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == 1) {
+    const long long T = tiles_before(a, U, a.B, blockIdx.x == 0 ? a.status : nullptr);
+    const long long n = min(T, static_cast<long long>(gridDim.x)), c = blockIdx.x;   // no empty range before n
+    TileRange r;
+    r.t0 = c < n ? T * c / n : 0;
+    r.t1 = c < n ? T * (c + 1) / n : 0;
+    r.b = 0;
+    r.cum = 0;
+    if (r.t0 < r.t1) find_tile(a, U, r.t0, r.b, r.cum);
+    if ((tid & 31) == 0) range = r;
+  }
+  grid_dep_launch();   // the merge kernel waits for this whole grid before it reads
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tS = tmem_base, tO = tmem_base + 256;
+  volatile int* abort_v = &abort_flag;
+  const TileRange rg = range;
+  const int nT = static_cast<int>(min(rg.t1 - rg.t0, static_cast<long long>(INT_MAX)));
+  TileIter it;
+  it.start(a, rg, U);
+  bool ok = true;
+
+  if (warp == TA_SOFTMAX / 32) {
+    // ---------------- copies: pieces in the order the MMA warp takes them, K(0), then K(t+1), V(t)
+    if ((tid & 31) == 0 && nT > 0) {
+      int pos = 0, seg = -1, t_end = 0;       // ring position; segment, first tile after it
+      long long vt_cum = 0;
+      (void)vt_cum;
+      auto slot_for = [&](uint8_t*& dst, uint64_t*& bar) {
+        const int s = pos % G::NS, use = pos / G::NS;
+        if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, WAIT_LIMIT_NS)) return false;
+        if (*abort_v) return false;
+        dst = dsm + G::QB * G::q_bytes + s * G::piece;
+        bar = &full[s];
+        mbar_arrive_expect_tx(bar, G::piece);
+        ++pos;
+        return true;
+      };
+      // the K side runs one tile ahead of the V side: V's plane and first slot of the tile before
+      int v_plane = 0, v_key = 0;
+      for (int t = 0; ok && t <= nT; ++t) {
+        int k_plane = 0, k_key = 0;
+        if (t < nT) {
+          if (t == t_end) {   // next segment: its query rows
+            it.next(a, RT);
+            t_end += it.tile1 - it.tile0;
+            ++seg;
+            const int qb = seg % G::QB, use = seg / G::QB;
+            if (use > 0 && !mbar_wait(&q_empty[qb], (use - 1) & 1, WAIT_LIMIT_NS)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&q_full[qb], G::q_bytes);
+            tma_load_4d(dsm + qb * G::q_bytes, &a.tm_q, 0, it.rt * 128, 0, it.b * a.Hkv + it.hk, &q_full[qb]);
+          }
+          k_plane = it.b * a.Hkv + it.hk;
+          k_key = (it.tile1 - (t_end - t)) * TREE_KEYS;
+          for (int p = 0; ok && p < G::pieces; ++p) {
+            uint8_t* dst;
+            uint64_t* bar;
+            ok = slot_for(dst, bar);
+            if (ok) tma_load_4d(dst, &a.tm_k, 0, k_key, p * G::k_blocks, k_plane, bar);
+          }
+        }
+        if (t > 0)
+          for (int p = 0; ok && p < G::pieces; ++p) {
+            uint8_t* dst;
+            uint64_t* bar;
+            ok = slot_for(dst, bar);
+            if (ok) tma_load_4d(dst, &a.tm_v, 0, v_key + p * G::v_keys, 0, v_plane, bar);
+          }
+        v_plane = k_plane;
+        v_key = k_key;
+      }
+      if (!ok) {
+        *abort_v = 1;
+        report_timeout(a.status, 0x710);
+      }
+      // no copy is in flight when the CTA leaves
+      for (int p = max(0, pos - G::NS); p < pos; ++p) mbar_wait(&full[p % G::NS], (p / G::NS) & 1, WAIT_LIMIT_NS);
+      for (int s = max(0, seg - G::QB + 1); s <= seg; ++s)
+        mbar_wait(&q_full[s % G::QB], (s / G::QB) & 1, WAIT_LIMIT_NS);
+    }
+  } else if (warp == TA_SOFTMAX / 32 + 1) {
+    // ---------------- MMAs
+    if ((tid & 31) == 0 && nT > 0) {
+      int pos = 0, seg = -1, t_end = 0;
+      auto piece = [&](uint32_t& addr) {   // the next piece, once it has landed
+        const int s = pos % G::NS;
+        if (!mbar_wait(&full[s], (pos / G::NS) & 1, WAIT_LIMIT_NS) || *abort_v) return false;
+        tc_fence_after();
+        addr = smem_u32(dsm + G::QB * G::q_bytes + s * G::piece);
+        return true;
+      };
+      auto issue_s = [&](int t) {
+        if (t == t_end) {
+          it.next(a, RT);
+          t_end += it.tile1 - it.tile0;
+          ++seg;
+          if (!mbar_wait(&q_full[seg % G::QB], (seg / G::QB) & 1, WAIT_LIMIT_NS)) return false;
+        }
+        // the columns still hold P(t - 2) until O += P(t - 2) V(t - 2) is done
+        if (t >= 2 && !mbar_wait(&bar_o[t & 1], ((t - 2) >> 1) & 1, WAIT_LIMIT_NS)) return false;
+        const uint32_t qa = smem_u32(dsm + (seg % G::QB) * G::q_bytes);
+#pragma unroll
+        for (int p = 0; p < G::pieces; ++p) {
+          uint32_t ka;
+          if (!piece(ka)) return false;
+#pragma unroll
+          for (int k = 0; k < G::k_blocks * 4; ++k)
+            mma_bf16(tS + (t & 1) * TREE_KEYS,
+                     smem_desc_sw128(qa + (p * G::k_blocks + (k >> 2)) * (128 * 128) + (k & 3) * 32, 16, 1024),
+                     smem_desc_sw128(ka + (k >> 2) * (TREE_KEYS * 128) + (k & 3) * 32, 16, 1024), IDESC_S,
+                     p > 0 || k > 0);
+          mma_commit(&empty[pos % G::NS]);
+          ++pos;
+        }
+        mma_commit(&bar_s[t & 1]);
+        if (t + 1 == t_end) mma_commit(&q_empty[seg % G::QB]);
+        return true;
+      };
+      TileIter vi = it;   // the V side: where segments begin
+      int v_end = 0, v_first = 0;
+      ok = issue_s(0);
+      for (int t = 0; ok && t < nT; ++t) {
+        if (t + 1 < nT) ok = issue_s(t + 1);
+        if (t == v_end) {
+          vi.next(a, RT);
+          v_first = t;
+          v_end += vi.tile1 - vi.tile0;
+        }
+        ok = ok && mbar_wait(&bar_p[t & 1], (t >> 1) & 1, WAIT_LIMIT_NS);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int p = 0; p < G::pieces; ++p) {
+          uint32_t va;
+          ok = piece(va);
+          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < G::v_keys / 16; ++k)
+            mma_bf16_ta(tO, tS + (t & 1) * TREE_KEYS + (p * (G::v_keys / 16) + k) * 8,
+                        smem_desc_sw128(va + k * 2048, G::v_keys * 128, 1024), IDESC_O,
+                        (t > v_first || p > 0 || k > 0) ? 1u : 0u);
+          mma_commit(&empty[pos % G::NS]);
+          ++pos;
+        }
+        mma_commit(&bar_o[t & 1]);
+      }
+      if (!ok) {
+        *abort_v = 1;
+        report_timeout(a.status, 0x711);
+      }
+      // every MMA issued has completed before tensor memory is freed
+      mma_commit(&fin_bar);
+      if (!mbar_wait(&fin_bar, 0, WAIT_LIMIT_NS)) report_timeout(a.status, 0x712);
+    }
+  } else {
+    // ---------------- softmax.  A warp whose wait gave up goes on without waiting (the named barriers
+    // need every warp) and stores nothing.
+    const int row = tid & 127, hh = tid >> 7, pw = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(pw * 32) << 16;
+    const float sl2 = a.scale * 1.4426950408889634f;   // scores in log2 units
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, WAIT_LIMIT_NS) && !*abort_v);
+      tc_fence_after();
+    };
+    int t = 0, nbound = 0;
+    while (it.next(a, RT)) {
+      const int Rv = min(128, R - it.rt * 128);
+      const bool work = pw * 32 < Rv;                  // this warp's rows are rows of the unit
+      const int rr = it.rt * 128 + row;                // row of the group: (head, token)
+      const int tok = rr % a.N, hq = it.hk * g + rr / a.N;
+      const uint32_t* words = a.mask ? a.mask + (static_cast<size_t>(it.b) * a.N + min(tok, a.N - 1)) * a.W : nullptr;
+      const int len = it.len, keys = len + a.N;
+      float ref = -INFINITY, l = 0.f;
+      bool spoilt = false;                             // a drafted value row that this row sees is not finite
+      for (int tile = it.tile0; tile < it.tile1; ++tile, ++t) {
+        const int key0 = tile * TREE_KEYS;
+        const bool boundary = key0 + TREE_KEYS > len;  // holds drafted slots or slots past them
+        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
+        if (boundary) {
+          // Values that a row does not see must not reach it through 0 * NaN: rows past the drafts, and
+          // drafted rows that are not finite, are zeroed where they landed.
+          const int pv = G::pieces * (min(t + 2, nT) + t);   // ring position of V(t)
+          for (int p = 0; p < G::pieces; ++p) wait(&full[(pv + p) % G::NS], ((pv + p) / G::NS) & 1);
+          const int key = key0 + row;
+          uint32_t(&bd)[4] = bad[nbound % 3];
+          if (key >= len && ok) {
+            const int vp = row / G::v_keys;
+            uint8_t* v0 = dsm + G::QB * G::q_bytes + ((pv + vp) % G::NS) * G::piece + (row - vp * G::v_keys) * 128;
+            constexpr int HB = DH == 64 ? 1 : DH / 128;      // feature blocks per thread (a half-row at dh = 64)
+            bool clear = key >= keys;
+            if (!clear) {
+#pragma unroll 1
+              for (int i = 0; i < (DH == 64 ? 4 : HB * 8); ++i) {
+                const uint4 x = *reinterpret_cast<const uint4*>(
+                    v0 + (DH == 64 ? hh * 64 + i * 16 : (hh * HB + (i >> 3)) * (G::v_keys * 128) + (i & 7) * 16));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  clear |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+              }
+              if (clear) atomicOr(&bd[row >> 5], 1u << (row & 31));
+            }
+          }
+          softmax_barrier();
+          if (key >= len && ok && (key >= keys || ((bd[row >> 5] >> (row & 31)) & 1u))) {
+            const int vp = row / G::v_keys;
+            uint8_t* v0 = dsm + G::QB * G::q_bytes + ((pv + vp) % G::NS) * G::piece + (row - vp * G::v_keys) * 128;
+            constexpr int HB = DH == 64 ? 1 : DH / 128;
+#pragma unroll 1
+            for (int i = 0; i < (DH == 64 ? 4 : HB * 8); ++i)
+              *reinterpret_cast<uint4*>(v0 + (DH == 64 ? hh * 64 + i * 16
+                                                       : (hh * HB + (i >> 3)) * (G::v_keys * 128) + (i & 7) * 16)) =
+                  make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+          if (tid < 4) bad[(nbound + 2) % 3][tid] = 0;
+          ++nbound;
+          const int j0 = key0 + 64 * hh - len;
+          vis[0] = seen_slots(words, tok, a.N, j0);
+          vis[1] = seen_slots(words, tok, a.N, j0 + 32);
+          if ((vis[0] & bd[2 * hh]) | (vis[1] & bd[2 * hh + 1])) spoilt = true;
+        }
+        wait(&bar_s[t & 1], (t >> 1) & 1);
+        const uint32_t tSt = tS + (t & 1) * TREE_KEYS + lanes;
+        if (work) {
+          uint32_t s[64];
+          tmem_ld32_nowait(tSt + 64 * hh, s);
+          tmem_ld32_nowait(tSt + 64 * hh + 32, s + 32);
+          tmem_wait_ld();
+          if (boundary) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (!((vis[e >> 5] >> (e & 31)) & 1u)) s[e] = 0xff800000u;   // -inf
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 64; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(s[e]));
+          const float mine = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          mx_sh[t & 1][hh][row] = mine;
+          pair_barrier(pw);   // also: both halves of the scores have left their columns
+          const float mx = fmaxf(mine, mx_sh[t & 1][hh ^ 1][row]) * sl2;
+          const float nref = mx > ref + TA_RESCALE || ref == -INFINITY ? fmaxf(mx, ref) : ref;
+          const float corr = nref == -INFINITY ? 1.f : exp2f(ref - nref);   // first visible slot: 0
+          const float off = nref == -INFINITY ? 0.f : nref;
+          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            const float p0 = ex2_approx(fmaf(__uint_as_float(s[e]), sl2, -off));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(s[e + 1]), sl2, -off));
+            ps[(e >> 1) & 3] += p0 + p1;
+            pk[e >> 1] = pack_bf16x2(p0, p1);
+          }
+          tmem_st32(tSt + 32 * hh, pk);
+          l = l * corr + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+          if (tile > it.tile0 && __any_sync(0xffffffffu, corr != 1.f)) {
+            wait(&bar_o[(t - 1) & 1], ((t - 1) >> 1) & 1);   // O holds the tiles before this one
+#pragma unroll 1
+            for (int c0 = hh * (DH / 2); c0 < (hh + 1) * (DH / 2); c0 += 32) {
+              uint32_t ov[32];
+              tmem_ld32_nowait(tO + lanes + c0, ov);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
+              tmem_st32(tO + lanes + c0, ov);
+            }
+          }
+          ref = nref;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(&bar_p[t & 1]);
+      }
+      // ---------------- the segment's rows
+      wait(&bar_o[(t - 1) & 1], ((t - 1) >> 1) & 1);
+      if (work) {
+        // the halves' sums; the sign says that a value row was not finite
+        float(&sums)[2][128] = mx_sh[t & 1];   // last read before this tile's barrier
+        sums[hh][row] = spoilt ? -l : l;
+        pair_barrier(pw);
+        const float l0 = sums[0][row], l1 = sums[1][row];
+        pair_barrier(pw);                      // before the next tile's maxima
+        const float lt = fabsf(l0) + fabsf(l1);
+        const float bad_v = signbit(l0) || signbit(l1) ? NAN : 0.f;
+        const bool whole = it.tile1 - it.tile0 == it.nb;
+        const bool mine = row < Rv && ok;
+        const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) + bad_v : 1.f;
+        __nv_bfloat16* orow = a.o + (static_cast<size_t>(it.b) * a.N + tok) * a.Hq * DH + static_cast<size_t>(hq) * DH;
+        const int slot = 2 * blockIdx.x + (it.first ? 0 : 1);
+        float* xrow = whole ? nullptr : a.scratch + (static_cast<size_t>(slot) * min(128, R) + row) * OLD;
+#pragma unroll 1
+        for (int c0 = hh * (DH / 2); c0 < (hh + 1) * (DH / 2); c0 += 32) {
+          uint32_t ov[32];
+          tmem_ld32_nowait(tO + lanes + c0, ov);
+          tmem_wait_ld();
+          if (!mine) continue;
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = pack_bf16x2(__uint_as_float(ov[e + 2 * i]) * inv, __uint_as_float(ov[e + 2 * i + 1]) * inv);
+              *reinterpret_cast<uint4*>(orow + c0 + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(xrow + c0 + e) = make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+          }
+        }
+        if (mine && hh == 0) {
+          if (!whole) {
+            *reinterpret_cast<float4*>(xrow + DH) = make_float4(ref, lt, bad_v, 0.f);
+          } else if (a.lse) {
+            a.lse[(static_cast<size_t>(it.b) * a.Hq + hq) * a.N + tok] =
+                ref == -INFINITY ? -INFINITY : (ref + log2f(lt)) * 0.6931471805599453f;
+          }
+        }
+        tc_fence_before();
+      }
+      it.first = 0;
+    }
+    if (!ok) {
+      *abort_v = 1;
+      if ((tid & 31) == 0) report_timeout(a.status, 0x713);
+    }
   }
   __syncthreads();
-  const float inv = poison ? NAN : l == 0.f ? 0.f : 1.f / l;
-  for (int e = 0; e < 2; ++e)
-    if (tid + 128 * e < a.dh)
-      a.o[(static_cast<size_t>(b) * a.N + n) * a.Hq * a.dh + hq * a.dh + tid + 128 * e] =
-          __float2bfloat16_rn(o[e] * inv);
-  if (a.lse && tid == 0) a.lse[row] = m == -INFINITY ? m : m + logf(l);
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
 }
 
-// One thread per slot.
-__global__ void __launch_bounds__(128) k_weights_rows(const __grid_constant__ TreeArgs a) {
-  __shared__ float q[256];
-  const int s = blockIdx.x * 128 + threadIdx.x, hk = blockIdx.y, b = blockIdx.z;
-  const int len = a.lens[b];
-  if (len < 0 || len > a.S_max - a.N) {
-    if (len > 0 && s == 0 && hk == 0) report_sample(a.status, CACHE_BAD_LEN, b);
-    return;
+// ------------------------------------------------------------------ merge
+// Joins the segments of units that lie on several CTAs.  `wpr` warps share a row (its segments strided
+// over them), 8 / wpr rows per CTA; grid (row groups, row tiles x KV heads, samples).
+constexpr int TM_WARPS = 8;
+
+template <int DH>
+__global__ void __launch_bounds__(TM_WARPS * 32) k_tree_merge(const __grid_constant__ TreeArgs a, int wpr) {
+  constexpr int OLD = DH + 4, VL = DH / 32;   // features per lane
+  __shared__ long long sh_T, sh_cum;
+  __shared__ float red[TM_WARPS][DH + 4];
+  const int g = a.Hq / a.Hkv, R = g * a.N, RT = (R + 127) >> 7, U = a.Hkv * RT;
+  const int b = blockIdx.z, u = blockIdx.y, rt = u % RT, hk = u / RT;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rpc = TM_WARPS / wpr;             // rows per CTA
+  const int Rv = min(128, R - rt * 128);
+  const int row = blockIdx.x * rpc + warp / wpr, sub = warp % wpr;
+  if (warp == 0) {
+    const long long T = tiles_before(a, U, a.B, nullptr);
+    if (lane == 0) sh_T = T;
+  } else if (warp == 1) {
+    const long long c = tiles_before(a, U, b, nullptr);
+    if (lane == 0) sh_cum = c;
   }
-  const int g = a.Hq / a.Hkv;
-  const size_t slot = (static_cast<size_t>(b) * a.Hkv + hk) * a.S_max + s;
-  float w = 0.f;
-  for (int r = 0; r < g * a.N; ++r) {
-    const size_t row = (static_cast<size_t>(b) * a.Hq + hk * g) * a.N + r;
-    const int n = r % a.N;
-    __syncthreads();
-    for (int d = threadIdx.x; d < a.dh; d += 128) q[d] = __bfloat162float(a.q[row * a.dh + d]) * a.scale;
-    __syncthreads();
-    const float lse = a.lse[row];
-    const bool counts = !a.use || ((a.use[static_cast<size_t>(b) * a.W + (n >> 5)] >> (n & 31)) & 1u);
-    if (counts && lse != -INFINITY && s < len + a.N && sees(a, b, n, len, s))
-      w += expf(dot_row(q, a.k + slot * a.dh, a.dh) - lse);
+  const int nb = sample_tiles(a, b);
+  __syncthreads();
+  grid_dep_wait();
+  if (nb == 0 || blockIdx.x * rpc >= Rv) return;
+  const long long T = sh_T, t0 = sh_cum + static_cast<long long>(u) * nb, t1 = t0 + nb;
+  // CTA c < n holds tiles [T c / n, T (c + 1) / n), at least one
+  const int n = static_cast<int>(min(T, static_cast<long long>(a.ctas)));
+  auto holder = [&](long long t) { return static_cast<int>(((t + 1) * n - 1) / T); };
+  const int c0 = holder(t0), c1 = holder(t1 - 1);
+  if (c0 == c1) return;   // one segment: written by k_tree_attn
+  // CTA c0's segment of this unit is its first one only if its range begins with it
+  auto part = [&](int c) {
+    const int s = 2 * c + (c == c0 && T * c / n != t0 ? 1 : 0);
+    return a.scratch + (static_cast<size_t>(s) * min(128, R) + row) * OLD;
+  };
+  float m = -INFINITY, l = 0.f, x = 0.f, o[VL];
+#pragma unroll
+  for (int e = 0; e < VL; ++e) o[e] = 0.f;
+  auto add = [&](float m2, float l2, float x2, const float* v) {
+    const float mn = fmaxf(m, m2);
+    if (mn == -INFINITY) return;
+    const float w0 = exp2f(m - mn), w1 = exp2f(m2 - mn);
+    m = mn;
+    l = l * w0 + l2 * w1;
+    x += x2;
+#pragma unroll
+    for (int e = 0; e < VL; ++e) o[e] = o[e] * w0 + v[e] * w1;
+  };
+  if (row < Rv) {
+    constexpr int UN = 4;   // segments in flight
+    for (int cb = c0 + sub; cb <= c1; cb += UN * wpr) {
+      float v[UN][VL];
+      float4 st[UN];
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        const int c = cb + i * wpr;
+        st[i] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        if (c <= c1) {
+          const float* p = part(c);
+          st[i] = *reinterpret_cast<const float4*>(p + DH);
+#pragma unroll
+          for (int e = 0; e < VL; e += 2)
+            *reinterpret_cast<float2*>(&v[i][e]) = *reinterpret_cast<const float2*>(p + (e / 2) * 64 + 2 * lane);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < UN; ++i)
+        if (cb + i * wpr <= c1) add(st[i].x, st[i].y, st[i].z, v[i]);
+    }
   }
-  if (s < len + a.N) a.acc[slot] = s < len ? a.acc[slot] + w : w;
+  if (wpr > 1) {
+#pragma unroll
+    for (int e = 0; e < VL; e += 2) *reinterpret_cast<float2*>(&red[warp][(e / 2) * 64 + 2 * lane]) = make_float2(o[e], o[e + 1]);
+    if (lane == 0) {
+      red[warp][DH] = m;
+      red[warp][DH + 1] = l;
+      red[warp][DH + 2] = x;
+    }
+    __syncthreads();
+    if (sub == 0)
+      for (int w = warp + 1; w < warp + wpr; ++w) {
+        float v[VL];
+#pragma unroll
+        for (int e = 0; e < VL; e += 2) *reinterpret_cast<float2*>(&v[e]) = *reinterpret_cast<float2*>(&red[w][(e / 2) * 64 + 2 * lane]);
+        add(red[w][DH], red[w][DH + 1], red[w][DH + 2], v);
+      }
+  }
+  if (row >= Rv || sub != 0) return;
+  const int rr = rt * 128 + row, tok = rr % a.N, hq = hk * g + rr / a.N;
+  const float inv = (l == 0.f ? 0.f : 1.f / l) + x;
+  __nv_bfloat16* orow = a.o + (static_cast<size_t>(b) * a.N + tok) * a.Hq * DH + static_cast<size_t>(hq) * DH;
+#pragma unroll
+  for (int e = 0; e < VL; e += 2)
+    *reinterpret_cast<uint32_t*>(orow + (e / 2) * 64 + 2 * lane) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+  if (a.lse && lane == 0)
+    a.lse[(static_cast<size_t>(b) * a.Hq + hq) * a.N + tok] =
+        m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int DH>
+cudaError_t launch_tree(TreeArgs& a, cudaStream_t s) {
+  using G = TreeGeom<DH>;
+  const int g = a.Hq / a.Hkv, R = g * a.N, RT = (R + 127) / 128;
+  const uint64_t planes = static_cast<uint64_t>(a.B) * a.Hkv;
+  if (!encode_rows_map(&a.tm_q, a.q, DH, R, R, planes, 128, DH / 64) ||
+      !encode_rows_map(&a.tm_k, a.k, DH, a.S_max, a.S_max, planes, TREE_KEYS, G::k_blocks) ||
+      !encode_rows_map(&a.tm_v, a.v, DH, a.S_max, a.S_max, planes, G::v_keys, DH / 64))
+    return cudaErrorInvalidValue;
+  k_tree_attn<DH><<<a.ctas, TA_THREADS, G::smem, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.S_max <= TREE_KEYS) return e;   // a unit of one tile is never split
+  // segments per unit if every sample is as long as can be
+  const int64_t units = static_cast<int64_t>(planes) * RT;
+  const int per = static_cast<int>(a.ctas / std::min<int64_t>(units, a.ctas)) + 1;
+  const int wpr = per > 32 ? 8 : per > 16 ? 4 : per > 8 ? 2 : 1;
+  const int rpc = TM_WARPS / wpr;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((std::min(R, 128) + rpc - 1) / rpc, a.Hkv * RT, a.B);
+  cfg.blockDim = dim3(TM_WARPS * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_tree_merge<DH>, a, wpr);
+}
+
+template <int DH>
+cudaError_t tree_init() {
+  return cudaFuncSetAttribute(k_tree_attn<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeGeom<DH>::smem);
 }
 
 }  // namespace
 
-size_t tree_scratch_bytes(int, int, int, int, int, int) { return 0; }
-
-cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s) {
-  k_tree_rows<<<dim3(a.N, a.Hq, a.B), 128, 0, s>>>(a);
-  return cudaGetLastError();
+size_t tree_scratch_bytes(int, int Hq, int Hkv, int N, int S_max, int dh) {
+  if (S_max <= TREE_KEYS) return 0;
+  return static_cast<size_t>(2) * TA_CTAS * std::min(128, Hq / Hkv * N) * (dh + 4) * 4;
 }
 
-cudaError_t launch_attention_weights(const TreeArgs& a, cudaStream_t s) {
-  k_weights_rows<<<dim3((a.S_max + 127) / 128, a.Hkv, a.B), 128, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_tree_attention(const TreeArgs& args, cudaStream_t s) {
+  TreeArgs a = args;
+  int dev = 0, nsm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  a.ctas = std::min(nsm, TA_CTAS);
+  return a.dh == 64 ? launch_tree<64>(a, s) : a.dh == 128 ? launch_tree<128>(a, s) : launch_tree<256>(a, s);
 }
 
-cudaError_t cache_ops_init() { return cache_moves_init(); }
+cudaError_t cache_ops_init() {
+  cudaError_t e;
+  if ((e = tree_init<64>()) != cudaSuccess || (e = tree_init<128>()) != cudaSuccess ||
+      (e = tree_init<256>()) != cudaSuccess)
+    return e;
+  return cache_moves_init();
+}
 
 }  // namespace tc
 }  // namespace fr
