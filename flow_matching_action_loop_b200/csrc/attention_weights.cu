@@ -1,56 +1,318 @@
-// The attention weight that each slot of a static KV cache received.
+// The attention weight that each slot of a static KV cache received (fr_attention_weights).
+//
+// With the log-sum-exp of every row known, slot s's weight is a sum over rows of independent terms,
+// exp(q k_s / sqrt(dh) - lse).  The scores are computed transposed, K Q^T: a lane of tensor memory is a
+// slot and a column a row, so that each thread sums the terms of one slot in registers and nothing is
+// exchanged but the two halves of the columns; there are no atomics.
+//
+// The 128-slot tiles of all (sample, KV head) pairs form one line, cut into equal ranges over the CTAs (one
+// per SM).  A CTA keeps up to 256 of the pair's rows in shared memory and streams its K tiles past them
+// (from the second 256 rows on out of the L2); a slot's sum is added to acc by the same thread each time.
+//   copy warp      query rows, K tiles by tensor map (128-byte swizzle) into a ring
+//   MMA warp       K(t) Q^T, 128 rows at a time, into one of four score buffers in tensor memory
+//   sum warps (8)  two threads per slot, half of the columns each: 2^(s - lse) in fp32
+#include <algorithm>
+
+#include "fr.h"
 #include "tree_device.h"
 
 namespace fr {
 namespace tc {
 namespace {
 
-// Whether token n sees slot s of sample b (len committed tokens).
-__device__ __forceinline__ bool sees(const TreeArgs& a, int b, int n, int len, int s) {
-  if (s < len) return true;
-  const int j = s - len;
-  if (j >= a.N) return false;
-  if (!a.mask) return j <= n;
-  return (a.mask[(static_cast<size_t>(b) * a.N + n) * a.W + (j >> 5)] >> (j & 31)) & 1u;
+using namespace fr::sm100;
+
+constexpr int AW_SUM = 256;
+constexpr int AW_THREADS = AW_SUM + 64;
+constexpr int AW_CHUNK = 128;               // rows per score buffer
+constexpr int AW_PASS = 2 * AW_CHUNK;       // rows held in shared memory
+constexpr int AW_BUFS = 4;                  // score buffers
+constexpr int AW_SLOTS = 10;                // ring slots at most
+constexpr int AW_SMEM = 224 * 1024;
+
+template <int DH>
+struct WeightGeom {
+  static constexpr int pieces = DH == 256 ? 2 : 1;                // per K tile, 64 or 128 features and more
+  static constexpr int piece = TREE_KEYS * DH * 2 / pieces;
+  static constexpr int blocks = DH / 64 / pieces;
+  static constexpr int q_bytes = AW_CHUNK * DH * 2;               // one chunk of rows
+};
+
+template <int DH>
+__global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_constant__ TreeArgs a) {
+  using G = WeightGeom<DH>;
+  extern __shared__ __align__(1024) uint8_t dsm[];
+  __shared__ uint64_t full[AW_SLOTS], empty[AW_SLOTS], q_full, q_empty, bar_s[AW_BUFS], bar_e[AW_BUFS], fin_bar;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  __shared__ TileRange range;
+  __shared__ __align__(16) float lse_sh[AW_PASS];   // in log2 units, +inf: a row that gives nothing
+  __shared__ float half_sh[2][128];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int g = a.Hq / a.Hkv, R = g * a.N;
+  const int passes = (R + AW_PASS - 1) / AW_PASS;
+  // the query rows of a pass take as many chunks as the largest pass has; the ring has the rest
+  const int q_chunks = R > AW_CHUNK ? 2 : 1;
+  const int NS = min(AW_SLOTS, (AW_SMEM - q_chunks * G::q_bytes) / G::piece);
+  uint8_t* ring = dsm + q_chunks * G::q_bytes;
+
+  if (tid == 0) {
+    for (int i = 0; i < AW_SLOTS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < AW_BUFS; ++i) {
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_e[i], AW_SUM / 32);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    mbar_init(&fin_bar, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == 1) {
+    const TileRange r = tile_range(a, a.Hkv);
+    if ((tid & 31) == 0) range = r;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tS = tmem_base;
+  volatile int* abort_v = &abort_flag;
+  const TileRange rg = range;
+  TileIter it;
+  it.start(a, rg, a.Hkv);
+  bool ok = true;
+  auto pass_rows = [&](int p) { return min(AW_PASS, R - p * AW_PASS); };
+
+  if (warp == AW_SUM / 32) {
+    // ---------------- copies
+    if ((tid & 31) == 0) {
+      int slot = 0, use = 0, q_use = 0, issued = 0;
+      while (ok && it.next(a, 1)) {
+        const int plane = it.b * a.Hkv + it.hk;
+        for (int p = 0; ok && p < passes; ++p) {
+          if (q_use > 0 && !mbar_wait(&q_empty, (q_use - 1) & 1, WAIT_LIMIT_NS)) {
+            ok = false;
+            break;
+          }
+          ++q_use;
+          const int nc = (pass_rows(p) + AW_CHUNK - 1) / AW_CHUNK;
+          mbar_arrive_expect_tx(&q_full, nc * G::q_bytes);
+          for (int c = 0; c < nc; ++c)
+            tma_load_4d(dsm + c * G::q_bytes, &a.tm_q, 0, p * AW_PASS + c * AW_CHUNK, 0, plane, &q_full);
+          for (int tile = it.tile0; ok && tile < it.tile1; ++tile)
+            for (int i = 0; i < G::pieces; ++i) {
+              if ((use > 0 && !mbar_wait(&empty[slot], (use - 1) & 1, WAIT_LIMIT_NS)) || *abort_v) {
+                ok = false;
+                break;
+              }
+              mbar_arrive_expect_tx(&full[slot], G::piece);
+              tma_load_4d(ring + slot * G::piece, &a.tm_k, 0, tile * TREE_KEYS, i * G::blocks, plane, &full[slot]);
+              ++issued;
+              if (++slot == NS) slot = 0, ++use;
+            }
+        }
+      }
+      if (!ok) {
+        *abort_v = 1;
+        report_timeout(a.status, 0x720);
+      }
+      // no copy is in flight when the CTA leaves
+      for (int i = max(0, issued - NS); i < issued; ++i) mbar_wait(&full[i % NS], (i / NS) & 1, WAIT_LIMIT_NS);
+      if (q_use > 0) mbar_wait(&q_full, (q_use - 1) & 1, WAIT_LIMIT_NS);
+    }
+  } else if (warp == AW_SUM / 32 + 1) {
+    // ---------------- MMAs
+    if ((tid & 31) == 0) {
+      int slot = 0, use = 0, q_use = 0, item = 0;
+      while (ok && it.next(a, 1)) {
+        for (int p = 0; ok && p < passes; ++p) {
+          ok = mbar_wait(&q_full, q_use & 1, WAIT_LIMIT_NS);
+          ++q_use;
+          const int rows = pass_rows(p), nc = (rows + AW_CHUNK - 1) / AW_CHUNK;
+          for (int tile = it.tile0; ok && tile < it.tile1; ++tile) {
+            for (int c = 0; c < nc; ++c, ++item) {
+              const int buf = item % AW_BUFS, nth = item / AW_BUFS;
+              if (nth > 0 && !mbar_wait(&bar_e[buf], (nth - 1) & 1, WAIT_LIMIT_NS)) ok = false;
+              const int cols = (min(AW_CHUNK, rows - c * AW_CHUNK) + 31) & ~31;
+              const uint32_t idesc = idesc_f32acc(FMT_BF16, 128, cols);
+              const uint32_t qa = smem_u32(dsm + c * G::q_bytes);
+              int s = slot, u = use;
+#pragma unroll
+              for (int i = 0; i < G::pieces; ++i) {
+                if (ok && c == 0) ok = mbar_wait(&full[s], u & 1, WAIT_LIMIT_NS) && !*abort_v;
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t ka = smem_u32(ring + s * G::piece);
+#pragma unroll
+                for (int k = 0; k < G::blocks * 4; ++k)
+                  mma_bf16(tS + buf * AW_CHUNK, smem_desc_sw128(ka + (k >> 2) * (TREE_KEYS * 128) + (k & 3) * 32, 16, 1024),
+                           smem_desc_sw128(qa + (i * G::blocks + (k >> 2)) * (AW_CHUNK * 128) + (k & 3) * 32, 16, 1024),
+                           idesc, i > 0 || k > 0);
+                if (c == nc - 1) mma_commit(&empty[s]);   // the tile's last rows
+                if (++s == NS) s = 0, ++u;
+              }
+              if (!ok) break;
+              mma_commit(&bar_s[buf]);
+            }
+            for (int i = 0; i < G::pieces; ++i)
+              if (++slot == NS) slot = 0, ++use;
+          }
+          if (ok) mma_commit(&q_empty);
+        }
+      }
+      if (!ok) {
+        *abort_v = 1;
+        report_timeout(a.status, 0x721);
+      }
+      // every MMA issued has completed before tensor memory is freed
+      mma_commit(&fin_bar);
+      if (!mbar_wait(&fin_bar, 0, WAIT_LIMIT_NS)) report_timeout(a.status, 0x722);
+    }
+  } else {
+    // ---------------- sums.  A warp whose wait gave up goes on without waiting (the named barriers need
+    // every warp) and stores nothing.
+    const int key = tid & 127, hh = tid >> 7, pw = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(pw * 32) << 16;
+    const float sl2 = a.scale * 1.4426950408889634f;   // scores in log2 units
+    int item = 0;
+    while (it.next(a, 1)) {
+      const int len = it.len, keys = len + a.N;
+      float* acc = a.acc + (static_cast<size_t>(it.b) * a.Hkv + it.hk) * a.S_max;
+      const float* lse = a.lse + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.hk) * g) * a.N;
+      for (int p = 0; p < passes; ++p) {
+        const int rows = pass_rows(p), nc = (rows + AW_CHUNK - 1) / AW_CHUNK, r0 = p * AW_PASS;
+        asm volatile("bar.sync 5, 256;" ::: "memory");   // the last pass has read its lse
+        {
+          float x = INFINITY;
+          if (tid < rows) {
+            const int n = (r0 + tid) % a.N;
+            const bool counts = !a.use || ((a.use[static_cast<size_t>(it.b) * a.W + (n >> 5)] >> (n & 31)) & 1u);
+            const float v = lse[r0 + tid];
+            if (counts && v != -INFINITY) x = v * 1.4426950408889634f;
+          }
+          lse_sh[tid] = x;
+        }
+        asm volatile("bar.sync 5, 256;" ::: "memory");
+        for (int tile = it.tile0; tile < it.tile1; ++tile) {
+          const int slot = tile * TREE_KEYS + key;
+          const bool boundary = (tile + 1) * TREE_KEYS > len;
+          // committed slots add to their sum; drafted ones begin with the first rows
+          const float before = hh == 0 && slot < keys && (slot < len || p > 0) ? acc[slot] : 0.f;
+          float w[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int c = 0; c < nc; ++c, ++item) {
+            const int buf = item % AW_BUFS;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bar_s[buf], (item / AW_BUFS) & 1, WAIT_LIMIT_NS) && !*abort_v);
+            tc_fence_after();
+            const int half = ((min(AW_CHUNK, rows - c * AW_CHUNK) + 31) & ~31) / 2;   // columns of this thread
+            const uint32_t ts = tS + buf * AW_CHUNK + lanes + hh * half;
+            const float* ls = lse_sh + c * AW_CHUNK + hh * half;
+            auto sum16 = [&](const uint32_t* s, int col) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 l4 = *reinterpret_cast<const float4*>(ls + col + e);
+                w[0] += ex2_approx(fmaf(__uint_as_float(s[e]), sl2, -l4.x));
+                w[1] += ex2_approx(fmaf(__uint_as_float(s[e + 1]), sl2, -l4.y));
+                w[2] += ex2_approx(fmaf(__uint_as_float(s[e + 2]), sl2, -l4.z));
+                w[3] += ex2_approx(fmaf(__uint_as_float(s[e + 3]), sl2, -l4.w));
+              }
+            };
+            if (!boundary) {
+              if (half == 64) {
+                uint32_t s[64];
+                tmem_ld32_nowait(ts, s);
+                tmem_ld32_nowait(ts + 32, s + 32);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if ((tid & 31) == 0) mbar_arrive(&bar_e[buf]);
+#pragma unroll
+                for (int col = 0; col < 64; col += 16) sum16(s + col, col);
+                continue;
+              }
+              for (int col = 0; col < half; col += 16) {
+                uint32_t s[16];
+                tmem_ld16_nowait(ts + col, s);
+                tmem_wait_ld();
+                sum16(s, col);
+              }
+            } else {
+              // a drafted slot counts for the rows whose token sees it
+              const int j = slot - len;
+              int n = (r0 + c * AW_CHUNK + hh * half) % a.N;
+              for (int col = 0; col < half; col += 16) {
+                uint32_t s[16];
+                tmem_ld16_nowait(ts + col, s);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  bool sees = j < 0;
+                  if (!sees && j < a.N)
+                    sees = a.mask ? (a.mask[(static_cast<size_t>(it.b) * a.N + n) * a.W + (j >> 5)] >> (j & 31)) & 1u : j <= n;
+                  const float l = ls[col + e];
+                  if (sees && l != INFINITY) w[e & 3] += ex2_approx(fmaf(__uint_as_float(s[e]), sl2, -l));
+                  if (++n == a.N) n = 0;
+                }
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(&bar_e[buf]);
+          }
+          const float mine = (w[0] + w[1]) + (w[2] + w[3]);
+          if (hh == 1) half_sh[tile & 1][key] = mine;
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + pw) : "memory");
+          if (hh == 0 && slot < keys && ok) acc[slot] = before + (mine + half_sh[tile & 1][key]);
+        }
+      }
+    }
+    if (!ok) {
+      *abort_v = 1;
+      if ((tid & 31) == 0) report_timeout(a.status, 0x723);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
 }
 
-__device__ __forceinline__ float dot_row(const float* q, const __nv_bfloat16* k, int dh) {
-  float s = 0.f;
-  for (int d = 0; d < dh; ++d) s = fmaf(q[d], __bfloat162float(k[d]), s);
-  return s;
-}
-
-// One thread per slot.
-__global__ void __launch_bounds__(128) k_weights_rows(const __grid_constant__ TreeArgs a) {
-  __shared__ float q[256];
-  const int s = blockIdx.x * 128 + threadIdx.x, hk = blockIdx.y, b = blockIdx.z;
-  const int len = a.lens[b];
-  if (len < 0 || len > a.S_max - a.N) {
-    if (len > 0 && s == 0 && hk == 0) report_sample(a.status, CACHE_BAD_LEN, b);
-    return;
-  }
-  const int g = a.Hq / a.Hkv;
-  const size_t slot = (static_cast<size_t>(b) * a.Hkv + hk) * a.S_max + s;
-  float w = 0.f;
-  for (int r = 0; r < g * a.N; ++r) {
-    const size_t row = (static_cast<size_t>(b) * a.Hq + hk * g) * a.N + r;
-    const int n = r % a.N;
-    __syncthreads();
-    for (int d = threadIdx.x; d < a.dh; d += 128) q[d] = __bfloat162float(a.q[row * a.dh + d]) * a.scale;
-    __syncthreads();
-    const float lse = a.lse[row];
-    const bool counts = !a.use || ((a.use[static_cast<size_t>(b) * a.W + (n >> 5)] >> (n & 31)) & 1u);
-    if (counts && lse != -INFINITY && s < len + a.N && sees(a, b, n, len, s))
-      w += expf(dot_row(q, a.k + slot * a.dh, a.dh) - lse);
-  }
-  if (s < len + a.N) a.acc[slot] = s < len ? a.acc[slot] + w : w;
+template <int DH>
+cudaError_t launch_weights(TreeArgs& a, cudaStream_t s) {
+  using G = WeightGeom<DH>;
+  const int R = a.Hq / a.Hkv * a.N;
+  const uint64_t planes = static_cast<uint64_t>(a.B) * a.Hkv;
+  if (!encode_rows_map(&a.tm_q, a.q, DH, R, R, planes, AW_CHUNK, DH / 64) ||
+      !encode_rows_map(&a.tm_k, a.k, DH, a.S_max, a.S_max, planes, TREE_KEYS, G::blocks))
+    return cudaErrorInvalidValue;
+  k_attn_weights<DH><<<a.ctas, AW_THREADS, AW_SMEM, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attention_weights(const TreeArgs& a, cudaStream_t s) {
-  k_weights_rows<<<dim3((a.S_max + 127) / 128, a.Hkv, a.B), 128, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t weights_init() {
+  cudaError_t e;
+  const auto at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if ((e = cudaFuncSetAttribute(k_attn_weights<64>, at, AW_SMEM)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(k_attn_weights<128>, at, AW_SMEM)) != cudaSuccess) return e;
+  return cudaFuncSetAttribute(k_attn_weights<256>, at, AW_SMEM);
+}
+
+cudaError_t launch_attention_weights(const TreeArgs& args, cudaStream_t s) {
+  TreeArgs a = args;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&a.ctas, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  return a.dh == 64 ? launch_weights<64>(a, s) : a.dh == 128 ? launch_weights<128>(a, s) : launch_weights<256>(a, s);
 }
 
 }  // namespace tc

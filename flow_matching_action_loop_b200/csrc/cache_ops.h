@@ -61,6 +61,7 @@ cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);
 cudaError_t launch_attention_weights(const TreeArgs& a, cudaStream_t s);
 cudaError_t launch_cache_commit(const MoveArgs& a, cudaStream_t s);
 cudaError_t launch_cache_evict(const MoveArgs& a, cudaStream_t s);
+cudaError_t weights_init();
 cudaError_t cache_moves_init();
 
 }  // namespace tc

@@ -48,84 +48,6 @@ struct TreeGeom {
   static constexpr int k_blocks = DH / 64 / pieces;             // feature blocks per K piece
 };
 
-// The line of tiles: sample b's units (KV head major, row tile minor), tiles minor.
-struct TileRange {
-  long long t0, t1, cum;   // this CTA's tiles; first tile of sample b
-  int b;                   // sample of t0
-};
-
-struct TileIter {
-  long long t, t1, cum;
-  int b, nb, U;
-  // segment
-  int len, hk, rt, tile0, tile1, first;
-  __device__ __forceinline__ void start(const TreeArgs& a, const TileRange& r, int U_) {
-    t = r.t0;
-    t1 = r.t1;
-    cum = r.cum;
-    b = r.b;
-    U = U_;
-    first = 1;
-    nb = t < t1 ? sample_tiles(a, b) : 0;
-  }
-  __device__ __forceinline__ bool next(const TreeArgs& a, int RT) {
-    if (t >= t1) return false;
-    while (t - cum >= static_cast<long long>(U) * nb) {
-      cum += static_cast<long long>(U) * nb;
-      nb = sample_tiles(a, ++b);
-    }
-    const int rel = static_cast<int>(t - cum), u = rel / nb;
-    len = a.lens[b];
-    hk = u / RT;
-    rt = u - hk * RT;
-    tile0 = rel - u * nb;
-    tile1 = static_cast<int>(min(static_cast<long long>(nb), tile0 + (t1 - t)));
-    t += tile1 - tile0;
-    return true;
-  }
-};
-
-// One warp: the number of tiles, the tiles before sample b_of (or, b_of < 0, the sample that holds tile
-// `at` and the tiles before it).
-__device__ __forceinline__ long long tiles_before(const TreeArgs& a, int U, int b_end, unsigned* status) {
-  const int lane = threadIdx.x & 31;
-  long long sum = 0;
-  for (int b0 = 0; b0 < b_end; b0 += 32) {
-    const int b = b0 + lane;
-    int n = 0;
-    if (b < b_end) {
-      n = sample_tiles(a, b);
-      if (status && n == 0 && a.lens[b] >= 0) report_sample(status, CACHE_BAD_LEN, b);
-    }
-    sum += n;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * U;
-}
-
-__device__ __forceinline__ void find_tile(const TreeArgs& a, int U, long long at, int& b_at, long long& cum_at) {
-  const int lane = threadIdx.x & 31;
-  long long cum = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const long long n = b0 + lane < a.B ? static_cast<long long>(sample_tiles(a, b0 + lane)) * U : 0;
-    long long incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, cum + incl > at);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      b_at = b0 + l;
-      cum_at = cum + __shfl_sync(0xffffffffu, incl - n, l);
-      return;
-    }
-    cum += __shfl_sync(0xffffffffu, incl, 31);
-  }
-}
-
 __device__ __forceinline__ void pair_barrier(int w) { asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory"); }
 __device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
 
@@ -167,14 +89,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
     tmem_relinquish();
   }
   if (warp == 1) {
-    const long long T = tiles_before(a, U, a.B, blockIdx.x == 0 ? a.status : nullptr);
-    const long long n = min(T, static_cast<long long>(gridDim.x)), c = blockIdx.x;   // no empty range before n
-    TileRange r;
-    r.t0 = c < n ? T * c / n : 0;
-    r.t1 = c < n ? T * (c + 1) / n : 0;
-    r.b = 0;
-    r.cum = 0;
-    if (r.t0 < r.t1) find_tile(a, U, r.t0, r.b, r.cum);
+    const TileRange r = tile_range(a, U);
     if ((tid & 31) == 0) range = r;
   }
   grid_dep_launch();   // the merge kernel waits for this whole grid before it reads
@@ -664,6 +579,7 @@ cudaError_t cache_ops_init() {
   if ((e = tree_init<64>()) != cudaSuccess || (e = tree_init<128>()) != cudaSuccess ||
       (e = tree_init<256>()) != cudaSuccess)
     return e;
+  if ((e = weights_init()) != cudaSuccess) return e;
   return cache_moves_init();
 }
 
