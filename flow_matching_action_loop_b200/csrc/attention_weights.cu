@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
     tmem_relinquish();
   }
   if (warp == 1) {
-    const TileRange r = tile_range(a, a.Hkv);
+    const TileRange r = tile_range(a, a.Hkv, blockIdx.x);
     if ((tid & 31) == 0) range = r;
   }
   tc_fence_before();
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
     // ---------------- copies
     if ((tid & 31) == 0) {
       int slot = 0, use = 0, q_use = 0, issued = 0;
-      while (ok && it.next(a, 1)) {
+      while (ok && it.next(a, 1, 1, 0)) {
         const int plane = it.b * a.Hkv + it.hk;
         for (int p = 0; ok && p < passes; ++p) {
           if (q_use > 0 && !mbar_wait(&q_empty, (q_use - 1) & 1, WAIT_LIMIT_NS)) {
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
     // ---------------- MMAs
     if ((tid & 31) == 0) {
       int slot = 0, use = 0, q_use = 0, item = 0;
-      while (ok && it.next(a, 1)) {
+      while (ok && it.next(a, 1, 1, 0)) {
         for (int p = 0; ok && p < passes; ++p) {
           ok = mbar_wait(&q_full, q_use & 1, WAIT_LIMIT_NS);
           ++q_use;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
     const uint32_t lanes = static_cast<uint32_t>(pw * 32) << 16;
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in log2 units
     int item = 0;
-    while (it.next(a, 1)) {
+    while (it.next(a, 1, 1, 0)) {
       const int len = it.len, keys = len + a.N;
       float* acc = a.acc + (static_cast<size_t>(it.b) * a.Hkv + it.hk) * a.S_max;
       const float* lse = a.lse + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.hk) * g) * a.N;
@@ -292,7 +292,7 @@ cudaError_t launch_weights(TreeArgs& a, cudaStream_t s) {
   if (!encode_rows_map(&a.tm_q, a.q, DH, R, R, planes, AW_CHUNK, DH / 64) ||
       !encode_rows_map(&a.tm_k, a.k, DH, a.S_max, a.S_max, planes, TREE_KEYS, G::blocks))
     return cudaErrorInvalidValue;
-  k_attn_weights<DH><<<a.ctas, AW_THREADS, AW_SMEM, s>>>(a);
+  k_attn_weights<DH><<<a.groups, AW_THREADS, AW_SMEM, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -308,9 +308,10 @@ cudaError_t weights_init() {
 
 cudaError_t launch_attention_weights(const TreeArgs& args, cudaStream_t s) {
   TreeArgs a = args;
+  a.rtg = 1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&a.ctas, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&a.groups, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   return a.dh == 64 ? launch_weights<64>(a, s) : a.dh == 128 ? launch_weights<128>(a, s) : launch_weights<256>(a, s);
 }

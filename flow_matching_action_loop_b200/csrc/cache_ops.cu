@@ -99,7 +99,7 @@ int fr_attention_tree(const void* q, const void* k, const void* v, const int32_t
                       size_t scratch_bytes, fr_stream_t stream) {
   const char* op = "fr_attention_tree";
   if (!q || !k || !v || !lens || !o || misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) ||
-      misaligned(o, 16) || misaligned(scratch, 16) || misaligned(lens, 4) || misaligned(mask, 4) ||
+      misaligned(o, 32) || misaligned(scratch, 16) || misaligned(lens, 4) || misaligned(mask, 4) ||
       misaligned(lse, 4)) {
     set_error("%s: NULL or misaligned tensor", op);
     return FR_ERR_ARG;

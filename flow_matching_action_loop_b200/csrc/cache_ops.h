@@ -32,7 +32,7 @@ struct TreeArgs {
   unsigned* status;
   int B, Hq, Hkv, N, W, S_max, dh;
   float scale;                 // 1/sqrt(dh)
-  int ctas;                    // attention: CTAs that share the tiles
+  int rtg, groups;             // CTAs per group (row tiles of a unit), groups that share the tiles
   CUtensorMap tm_q, tm_k, tm_v;   // written by the launchers
 };
 

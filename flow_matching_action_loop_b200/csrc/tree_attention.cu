@@ -5,14 +5,19 @@
 // All units' tiles form one line that the CTAs (one per SM) cut into equal ranges, whatever the samples'
 // lengths: a CTA runs the segments of units that lie in its range one after the other.  A segment that is
 // its whole unit writes o and lse; one that is part of a unit writes its rows (O, reference, sum) to the
-// scratch, and k_tree_merge, chained behind, joins them.
+// scratch, and k_tree_merge, chained behind, joins them.  The CTAs that run the row tiles of one KV head do
+// so side by side over the same range of keys (with a range of its own for each, the tiles came from HBM
+// 2.6 times at 6 x 33000 slots and four row tiles).
 //
 // Inside a CTA, per tile t:
 //   copy warp     K(t+1), V(t) by tensor map (128-byte swizzle) into a ring of shared-memory slots
 //   MMA warp      S(t+1) = Q K(t+1)^T, then O += P(t) V(t): tcgen05, fp32 in tensor memory; P is the A
-//                 operand from tensor memory, in the columns of the scores it came from
+//                 operand from tensor memory
 //   softmax warps (8) two threads per row, 64 slots each: running maximum and sum in fp32, P = 2^(s - ref)
-// so the tensor core works on S(t+1) and P(t-1) V(t-1) while the softmax of tile t runs.  The reference
+// The scores leave their columns for registers at the start of a tile's softmax, so the tensor core works on
+// P(t-1) V(t-1) and S(t+1) while the softmax of tile t runs: it waits for neither the other's end (with P
+// in the columns of the scores, S(t+1) waited for P(t-1) V(t-1): 1.97 us a tile at dh = 256 instead of
+// the 1.54 us of the products).  The reference
 // of a row's exponentials moves only when its maximum has grown by more than 2^8 (P stays below 2^8, O and
 // the sum keep one reference, O / sum is unchanged): O is rescaled rarely.
 // P is rounded to bf16, the tensor core's operand type: half a bf16 step per weight, as much as the
@@ -48,6 +53,13 @@ struct TreeGeom {
   static constexpr int k_blocks = DH / 64 / pieces;             // feature blocks per K piece
 };
 
+// 32 bytes, a whole sector, to a 16-byte aligned address that is a multiple of 32 past o's rows.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 __device__ __forceinline__ void pair_barrier(int w) { asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory"); }
 __device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
 
@@ -55,181 +67,215 @@ template <int DH>
 __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_constant__ TreeArgs a) {
   using G = TreeGeom<DH>;
   extern __shared__ __align__(1024) uint8_t dsm[];
-  __shared__ uint64_t full[G::NS], empty[G::NS], q_full[2], q_empty[2], bar_s[2], bar_o[2], bar_p[2], fin_bar;
+  __shared__ uint64_t full[G::NS], empty[G::NS], q_full[2], q_empty[2], bar_s, bar_l, bar_o[2], bar_p[2], fin_bar;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  __shared__ TileRange range;
+  __shared__ TileIter first_seg;           // its segment: the first
+  __shared__ int any_seg;
   __shared__ float mx_sh[2][2][128];       // [tile parity][half][row]; a segment's sums at its end
   __shared__ uint32_t bad[3][4];           // drafted value rows of a tile that are not finite
   constexpr uint32_t IDESC_S = idesc_f32acc(FMT_BF16, 128, TREE_KEYS);
   constexpr uint32_t IDESC_O = idesc_f32acc(FMT_BF16, 128, DH) | IDESC_B_MN_MAJOR;
   constexpr int OLD = DH + 4;              // floats per partial row: O, reference, sum, NaN if spoilt
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int g = a.Hq / a.Hkv, R = g * a.N, RT = (R + 127) >> 7, U = a.Hkv * RT;
+  const int g = a.Hq / a.Hkv, R = g * a.N, RT = (R + 127) >> 7, NB = (RT + a.rtg - 1) / a.rtg;
+  const int grp = blockIdx.x / a.rtg, r_in = blockIdx.x - grp * a.rtg;
+  uint8_t* ring = dsm + G::QB * G::q_bytes;
+  volatile int* abort_v = &abort_flag;
+  bool ok = true;
 
-  if (tid == 0) {
-    for (int i = 0; i < G::NS; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+  // the copies' state: next ring position, segments begun
+  int pos = 0, seg = -1;
+  auto load_q = [&](const TileIter& it) {
+    ++seg;
+    const int qb = seg % G::QB, use = seg / G::QB;
+    if (use > 0 && !mbar_wait(&q_empty[qb], (use - 1) & 1, WAIT_LIMIT_NS)) return false;
+    mbar_arrive_expect_tx(&q_full[qb], G::q_bytes);
+    tma_load_4d(dsm + qb * G::q_bytes, &a.tm_q, 0, it.rt * 128, 0, it.b * a.Hkv + it.hk, &q_full[qb]);
+    return true;
+  };
+  auto load_piece = [&](const CUtensorMap* tm, int key, int block, int plane) {
+    const int s = pos % G::NS, use = pos / G::NS;
+    if ((use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, WAIT_LIMIT_NS)) || *abort_v) return false;
+    mbar_arrive_expect_tx(&full[s], G::piece);
+    tma_load_4d(ring + s * G::piece, tm, 0, key, block, plane, &full[s]);
+    ++pos;
+    return true;
+  };
+  auto load_k = [&](const TileIter& it, int tile) {
+    for (int p = 0; p < G::pieces; ++p)
+      if (!load_piece(&a.tm_k, tile * TREE_KEYS, p * G::k_blocks, it.b * a.Hkv + it.hk)) return false;
+    return true;
+  };
+
+  // The copy warp finds the CTA's tiles and starts the first copies while warp 0 allocates tensor memory.
+  if (warp == TA_SOFTMAX / 32) {
+    if ((tid & 31) == 0) {
+      for (int i = 0; i < G::NS; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&q_full[i], 1);
+        mbar_init(&q_empty[i], 1);
+        mbar_init(&bar_o[i], 1);
+        mbar_init(&bar_p[i], TA_SOFTMAX / 32);
+      }
+      mbar_init(&bar_s, 1);
+      mbar_init(&bar_l, TA_SOFTMAX / 32);
+      mbar_init(&fin_bar, 1);
+      abort_flag = 0;
+      fence_mbar_init();
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
-      mbar_init(&bar_s[i], 1);
-      mbar_init(&bar_o[i], 1);
-      mbar_init(&bar_p[i], TA_SOFTMAX / 32);
+    __syncwarp();
+    const TileRange r = tile_range(a, a.Hkv * NB, grp);
+    if ((tid & 31) == 0) {
+      TileIter it;
+      it.start(a, r, a.Hkv * NB);
+      any_seg = it.next(a, RT, NB, r_in);
+      if (any_seg) {
+        load_q(it);
+        load_k(it, it.tile0);
+      }
+      first_seg = it;
     }
-    mbar_init(&fin_bar, 1);
-    abort_flag = 0;
-    fence_mbar_init();
   }
   if (tid < 12) bad[tid >> 2][tid & 3] = 0;
   if (warp == 0) {
     tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
   }
-  if (warp == 1) {
-    const TileRange r = tile_range(a, U);
-    if ((tid & 31) == 0) range = r;
-  }
   grid_dep_launch();   // the merge kernel waits for this whole grid before it reads
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tS = tmem_base, tO = tmem_base + 256;
-  volatile int* abort_v = &abort_flag;
-  const TileRange rg = range;
-  const int nT = static_cast<int>(min(rg.t1 - rg.t0, static_cast<long long>(INT_MAX)));
-  TileIter it;
-  it.start(a, rg, U);
-  bool ok = true;
+  // tensor memory: scores (128 columns), two P tiles (64 each), O (dh)
+  const uint32_t tS = tmem_base, tP = tmem_base + 128, tO = tmem_base + 256;
+  TileIter it = first_seg;
+  bool more = any_seg != 0;
 
   if (warp == TA_SOFTMAX / 32) {
     // ---------------- copies: pieces in the order the MMA warp takes them, K(0), then K(t+1), V(t)
-    if ((tid & 31) == 0 && nT > 0) {
-      int pos = 0, seg = -1, t_end = 0;       // ring position; segment, first tile after it
-      long long vt_cum = 0;
-      (void)vt_cum;
-      auto slot_for = [&](uint8_t*& dst, uint64_t*& bar) {
-        const int s = pos % G::NS, use = pos / G::NS;
-        if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, WAIT_LIMIT_NS)) return false;
-        if (*abort_v) return false;
-        dst = dsm + G::QB * G::q_bytes + s * G::piece;
-        bar = &full[s];
-        mbar_arrive_expect_tx(bar, G::piece);
-        ++pos;
-        return true;
-      };
-      // the K side runs one tile ahead of the V side: V's plane and first slot of the tile before
-      int v_plane = 0, v_key = 0;
-      for (int t = 0; ok && t <= nT; ++t) {
-        int k_plane = 0, k_key = 0;
-        if (t < nT) {
-          if (t == t_end) {   // next segment: its query rows
-            it.next(a, RT);
-            t_end += it.tile1 - it.tile0;
-            ++seg;
-            const int qb = seg % G::QB, use = seg / G::QB;
-            if (use > 0 && !mbar_wait(&q_empty[qb], (use - 1) & 1, WAIT_LIMIT_NS)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(&q_full[qb], G::q_bytes);
-            tma_load_4d(dsm + qb * G::q_bytes, &a.tm_q, 0, it.rt * 128, 0, it.b * a.Hkv + it.hk, &q_full[qb]);
-          }
-          k_plane = it.b * a.Hkv + it.hk;
-          k_key = (it.tile1 - (t_end - t)) * TREE_KEYS;
-          for (int p = 0; ok && p < G::pieces; ++p) {
-            uint8_t* dst;
-            uint64_t* bar;
-            ok = slot_for(dst, bar);
-            if (ok) tma_load_4d(dst, &a.tm_k, 0, k_key, p * G::k_blocks, k_plane, bar);
-          }
+    if ((tid & 31) == 0 && more) {
+      int tile = it.tile0;   // K(t) has been issued
+      for (;;) {
+        const int v_plane = it.b * a.Hkv + it.hk, v_key = tile * TREE_KEYS;
+        if (++tile == it.tile1) {
+          more = it.next(a, RT, NB, r_in);
+          tile = it.tile0;
+          if (more) ok = load_q(it);
         }
-        if (t > 0)
-          for (int p = 0; ok && p < G::pieces; ++p) {
-            uint8_t* dst;
-            uint64_t* bar;
-            ok = slot_for(dst, bar);
-            if (ok) tma_load_4d(dst, &a.tm_v, 0, v_key + p * G::v_keys, 0, v_plane, bar);
-          }
-        v_plane = k_plane;
-        v_key = k_key;
+        if (more) ok = ok && load_k(it, tile);
+        else pos += G::pieces;   // V(t) is at position pieces * (2 t + 2) for the last tile too
+        for (int p = 0; ok && p < G::pieces; ++p) ok = load_piece(&a.tm_v, v_key + p * G::v_keys, 0, v_plane);
+        if (!ok || !more) break;
       }
       if (!ok) {
         *abort_v = 1;
         report_timeout(a.status, 0x710);
       }
-      // no copy is in flight when the CTA leaves
-      for (int p = max(0, pos - G::NS); p < pos; ++p) mbar_wait(&full[p % G::NS], (p / G::NS) & 1, WAIT_LIMIT_NS);
+      // no copy is in flight when the CTA leaves (a position that was left out waits for the slot's last use)
+      for (int p = max(0, pos - G::NS); p < pos; ++p) {
+        const bool skipped = !more && p >= pos - 2 * G::pieces && p < pos - G::pieces && ok;
+        if (!skipped) mbar_wait(&full[p % G::NS], (p / G::NS) & 1, WAIT_LIMIT_NS);
+      }
       for (int s = max(0, seg - G::QB + 1); s <= seg; ++s)
         mbar_wait(&q_full[s % G::QB], (s / G::QB) & 1, WAIT_LIMIT_NS);
     }
   } else if (warp == TA_SOFTMAX / 32 + 1) {
     // ---------------- MMAs
-    if ((tid & 31) == 0 && nT > 0) {
-      int pos = 0, seg = -1, t_end = 0;
-      auto piece = [&](uint32_t& addr) {   // the next piece, once it has landed
-        const int s = pos % G::NS;
-        if (!mbar_wait(&full[s], (pos / G::NS) & 1, WAIT_LIMIT_NS) || *abort_v) return false;
-        tc_fence_after();
-        addr = smem_u32(dsm + G::QB * G::q_bytes + s * G::piece);
-        return true;
+    if ((tid & 31) == 0 && more) {
+      // The products of S(t+1) and of P(t) V(t) alternate.  What the next ones wait for is tested before the
+      // last of the present ones are issued, so that no barrier's latency lies between them.
+      int mpos = 0, mseg = -1, tile = it.tile0;   // ring position; S side: segment, tile of segment `it`
+      auto landed = [&](int p) { return mbar_test(&full[(mpos + p) % G::NS], ((mpos + p) / G::NS) & 1); };
+      auto wait_pieces = [&]() {
+        for (int p = 0; p < G::pieces; ++p)
+          if (!mbar_wait(&full[(mpos + p) % G::NS], ((mpos + p) / G::NS) & 1, WAIT_LIMIT_NS)) return false;
+        return !*abort_v;
       };
-      auto issue_s = [&](int t) {
-        if (t == t_end) {
-          it.next(a, RT);
-          t_end += it.tile1 - it.tile0;
-          ++seg;
-          if (!mbar_wait(&q_full[seg % G::QB], (seg / G::QB) & 1, WAIT_LIMIT_NS)) return false;
+      bool more_s = true, s_begins = true;
+      auto advance_s = [&]() {   // the next tile of the S side
+        s_begins = false;
+        if (++tile == it.tile1) {
+          more_s = it.next(a, RT, NB, r_in);
+          tile = it.tile0;
+          s_begins = true;
         }
-        // the columns still hold P(t - 2) until O += P(t - 2) V(t - 2) is done
-        if (t >= 2 && !mbar_wait(&bar_o[t & 1], ((t - 2) >> 1) & 1, WAIT_LIMIT_NS)) return false;
-        const uint32_t qa = smem_u32(dsm + (seg % G::QB) * G::q_bytes);
+      };
+      auto s_wait = [&](int t) {
+        if (s_begins && !mbar_wait(&q_full[(mseg + 1) % G::QB], ((mseg + 1) / G::QB) & 1, WAIT_LIMIT_NS)) return false;
+        if (t > 0 && !mbar_wait(&bar_l, (t - 1) & 1, WAIT_LIMIT_NS)) return false;   // S(t - 1) has been read
+        return wait_pieces();
+      };
+      // Returns whether P(t - 1) and V(t - 1) are there.
+      auto issue_s = [&](int t) {
+        if (s_begins) ++mseg;
+        tc_fence_after();
+        const uint32_t qa = smem_u32(dsm + (mseg % G::QB) * G::q_bytes);
+        bool r = false;
 #pragma unroll
         for (int p = 0; p < G::pieces; ++p) {
-          uint32_t ka;
-          if (!piece(ka)) return false;
+          const uint32_t ka = smem_u32(ring + ((mpos + p) % G::NS) * G::piece);
 #pragma unroll
-          for (int k = 0; k < G::k_blocks * 4; ++k)
-            mma_bf16(tS + (t & 1) * TREE_KEYS,
-                     smem_desc_sw128(qa + (p * G::k_blocks + (k >> 2)) * (128 * 128) + (k & 3) * 32, 16, 1024),
+          for (int k = 0; k < G::k_blocks * 4; ++k) {
+            if (p == G::pieces - 1 && k == G::k_blocks * 4 - 2 && t > 0) {
+              r = mbar_test(&bar_p[(t - 1) & 1], ((t - 1) >> 1) & 1);
+              for (int i = 0; i < G::pieces; ++i) r &= landed(G::pieces + i);
+            }
+            mma_bf16(tS, smem_desc_sw128(qa + (p * G::k_blocks + (k >> 2)) * (128 * 128) + (k & 3) * 32, 16, 1024),
                      smem_desc_sw128(ka + (k >> 2) * (TREE_KEYS * 128) + (k & 3) * 32, 16, 1024), IDESC_S,
                      p > 0 || k > 0);
-          mma_commit(&empty[pos % G::NS]);
-          ++pos;
+          }
+          mma_commit(&empty[(mpos + p) % G::NS]);
         }
-        mma_commit(&bar_s[t & 1]);
-        if (t + 1 == t_end) mma_commit(&q_empty[seg % G::QB]);
-        return true;
+        mma_commit(&bar_s);
+        if (tile + 1 == it.tile1) mma_commit(&q_empty[mseg % G::QB]);
+        mpos += G::pieces;
+        return r;
       };
-      TileIter vi = it;   // the V side: where segments begin
-      int v_end = 0, v_first = 0;
-      ok = issue_s(0);
-      for (int t = 0; ok && t < nT; ++t) {
-        if (t + 1 < nT) ok = issue_s(t + 1);
-        if (t == v_end) {
-          vi.next(a, RT);
-          v_first = t;
-          v_end += vi.tile1 - vi.tile0;
+      bool v_begins = true, s_ok = false;   // V(t) is a segment's first; S(t + 1) can be issued
+      int keys_v = it.len + a.N - tile * TREE_KEYS;
+      ok = s_wait(0);
+      if (ok) issue_s(0);
+      for (int t = 0; ok; ++t) {
+        advance_s();
+        bool pv_ok = false;
+        const int keys_s = more_s ? it.len + a.N - tile * TREE_KEYS : 0;
+        if (more_s) {
+          ok = s_ok || s_wait(t + 1);
+          if (!ok) break;
+          pv_ok = issue_s(t + 1);
+        } else {
+          mpos += G::pieces;
         }
-        ok = ok && mbar_wait(&bar_p[t & 1], (t >> 1) & 1, WAIT_LIMIT_NS);
+        if (!pv_ok) ok = mbar_wait(&bar_p[t & 1], (t >> 1) & 1, WAIT_LIMIT_NS) && wait_pieces();
         if (!ok) break;
         tc_fence_after();
+        const int steps = min(TREE_KEYS, keys_v + 15) / 16;   // of 16 slots: those that hold slots in use
+        s_ok = false;
 #pragma unroll
         for (int p = 0; p < G::pieces; ++p) {
-          uint32_t va;
-          ok = piece(va);
-          if (!ok) break;
+          const uint32_t va = smem_u32(ring + ((mpos + p) % G::NS) * G::piece);
 #pragma unroll
-          for (int k = 0; k < G::v_keys / 16; ++k)
-            mma_bf16_ta(tO, tS + (t & 1) * TREE_KEYS + (p * (G::v_keys / 16) + k) * 8,
-                        smem_desc_sw128(va + k * 2048, G::v_keys * 128, 1024), IDESC_O,
-                        (t > v_first || p > 0 || k > 0) ? 1u : 0u);
-          mma_commit(&empty[pos % G::NS]);
-          ++pos;
+          for (int k = 0; k < G::v_keys / 16; ++k) {
+            const int step = p * (G::v_keys / 16) + k;
+            if (step == TREE_KEYS / 16 - 1 && more_s && tile + 1 < it.tile1) {
+              // S(t + 2) follows in the same segment
+              s_ok = mbar_test(&bar_l, (t + 1) & 1);
+              for (int i = 0; i < G::pieces; ++i) s_ok &= landed(G::pieces + i);
+            }
+            if (step < steps)
+              mma_bf16_ta(tO, tP + (t & 1) * 64 + step * 8, smem_desc_sw128(va + k * 2048, G::v_keys * 128, 1024), IDESC_O,
+                          (!v_begins || step > 0) ? 1u : 0u);
+          }
+          mma_commit(&empty[(mpos + p) % G::NS]);
         }
         mma_commit(&bar_o[t & 1]);
+        mpos += G::pieces;
+        if (!more_s) break;
+        v_begins = s_begins;
+        keys_v = keys_s;
       }
       if (!ok) {
         *abort_v = 1;
@@ -250,7 +296,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
       tc_fence_after();
     };
     int t = 0, nbound = 0;
-    while (it.next(a, RT)) {
+    for (; more; more = it.next(a, RT, NB, r_in)) {
       const int Rv = min(128, R - it.rt * 128);
       const bool work = pw * 32 < Rv;                  // this warp's rows are rows of the unit
       const int rr = it.rt * 128 + row;                // row of the group: (head, token)
@@ -264,56 +310,21 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         const bool boundary = key0 + TREE_KEYS > len;  // holds drafted slots or slots past them
         uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
         if (boundary) {
-          // Values that a row does not see must not reach it through 0 * NaN: rows past the drafts, and
-          // drafted rows that are not finite, are zeroed where they landed.
-          const int pv = G::pieces * (min(t + 2, nT) + t);   // ring position of V(t)
-          for (int p = 0; p < G::pieces; ++p) wait(&full[(pv + p) % G::NS], ((pv + p) / G::NS) & 1);
-          const int key = key0 + row;
-          uint32_t(&bd)[4] = bad[nbound % 3];
-          if (key >= len && ok) {
-            const int vp = row / G::v_keys;
-            uint8_t* v0 = dsm + G::QB * G::q_bytes + ((pv + vp) % G::NS) * G::piece + (row - vp * G::v_keys) * 128;
-            constexpr int HB = DH == 64 ? 1 : DH / 128;      // feature blocks per thread (a half-row at dh = 64)
-            bool clear = key >= keys;
-            if (!clear) {
-#pragma unroll 1
-              for (int i = 0; i < (DH == 64 ? 4 : HB * 8); ++i) {
-                const uint4 x = *reinterpret_cast<const uint4*>(
-                    v0 + (DH == 64 ? hh * 64 + i * 16 : (hh * HB + (i >> 3)) * (G::v_keys * 128) + (i & 7) * 16));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  clear |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-              }
-              if (clear) atomicOr(&bd[row >> 5], 1u << (row & 31));
-            }
-          }
-          softmax_barrier();
-          if (key >= len && ok && (key >= keys || ((bd[row >> 5] >> (row & 31)) & 1u))) {
-            const int vp = row / G::v_keys;
-            uint8_t* v0 = dsm + G::QB * G::q_bytes + ((pv + vp) % G::NS) * G::piece + (row - vp * G::v_keys) * 128;
-            constexpr int HB = DH == 64 ? 1 : DH / 128;
-#pragma unroll 1
-            for (int i = 0; i < (DH == 64 ? 4 : HB * 8); ++i)
-              *reinterpret_cast<uint4*>(v0 + (DH == 64 ? hh * 64 + i * 16
-                                                       : (hh * HB + (i >> 3)) * (G::v_keys * 128) + (i & 7) * 16)) =
-                  make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-          }
-          if (tid < 4) bad[(nbound + 2) % 3][tid] = 0;
-          ++nbound;
           const int j0 = key0 + 64 * hh - len;
           vis[0] = seen_slots(words, tok, a.N, j0);
           vis[1] = seen_slots(words, tok, a.N, j0 + 32);
-          if ((vis[0] & bd[2 * hh]) | (vis[1] & bd[2 * hh + 1])) spoilt = true;
         }
-        wait(&bar_s[t & 1], (t >> 1) & 1);
-        const uint32_t tSt = tS + (t & 1) * TREE_KEYS + lanes;
+        wait(&bar_s, t & 1);
+        uint32_t s[64];
         if (work) {
-          uint32_t s[64];
-          tmem_ld32_nowait(tSt + 64 * hh, s);
-          tmem_ld32_nowait(tSt + 64 * hh + 32, s + 32);
+          tmem_ld32_nowait(tS + lanes + 64 * hh, s);
+          tmem_ld32_nowait(tS + lanes + 64 * hh + 32, s + 32);
           tmem_wait_ld();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(&bar_l);
+        if (work) {
           if (boundary) {
 #pragma unroll
             for (int e = 0; e < 64; ++e)
@@ -321,25 +332,32 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
           }
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 64; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(s[e]));
+          for (int e = 0; e < 64; e += 2) {
+            float& m = m4[(e >> 1) & 3];
+            m = max3(m, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          }
           const float mine = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           mx_sh[t & 1][hh][row] = mine;
-          pair_barrier(pw);   // also: both halves of the scores have left their columns
+          pair_barrier(pw);
           const float mx = fmaxf(mine, mx_sh[t & 1][hh ^ 1][row]) * sl2;
           const float nref = mx > ref + TA_RESCALE || ref == -INFINITY ? fmaxf(mx, ref) : ref;
           const float corr = nref == -INFINITY ? 1.f : exp2f(ref - nref);   // first visible slot: 0
           const float off = nref == -INFINITY ? 0.f : nref;
-          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sl22 = pack_f32x2(sl2, sl2), off2 = pack_f32x2(-off, -off);
+          uint64_t ps[2] = {0, 0};
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(s[e]), sl2, -off));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(s[e + 1]), sl2, -off));
-            ps[(e >> 1) & 3] += p0 + p1;
+            const float2 x = unpack_f32x2(
+                fma_f32x2(pack_f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl22, off2));
+            const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+            ps[(e >> 1) & 1] = add_f32x2(ps[(e >> 1) & 1], pack_f32x2(p0, p1));
             pk[e >> 1] = pack_bf16x2(p0, p1);
           }
-          tmem_st32(tSt + 32 * hh, pk);
-          l = l * corr + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+          if (t >= 2) wait(&bar_o[t & 1], ((t - 2) >> 1) & 1);   // P(t - 2) has been read
+          tmem_st32(tP + (t & 1) * 64 + lanes + 32 * hh, pk);
+          const float2 pt = unpack_f32x2(add_f32x2(ps[0], ps[1]));
+          l = l * corr + (pt.x + pt.y);
           if (tile > it.tile0 && __any_sync(0xffffffffu, corr != 1.f)) {
             wait(&bar_o[(t - 1) & 1], ((t - 1) >> 1) & 1);   // O holds the tiles before this one
 #pragma unroll 1
@@ -354,6 +372,51 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
           }
           ref = nref;
           tmem_wait_st();
+        }
+        if (boundary) {
+          // Values that a row does not see must not reach it through 0 * NaN: drafted rows that are not
+          // finite, and the rows past the drafts in the last step of 16 slots that the product takes, are
+          // zeroed where they landed.
+          const int pv = G::pieces * (2 * t + 2);            // ring position of V(t)
+          for (int p = 0; p < G::pieces; ++p) wait(&full[(pv + p) % G::NS], ((pv + p) / G::NS) & 1);
+          constexpr int CPR = DH / 8;                        // 16-byte words per row
+          auto word = [&](int r, int c) {
+            const int vp = r / G::v_keys;
+            return reinterpret_cast<uint4*>(ring + ((pv + vp) % G::NS) * G::piece +
+                                            (c >> 3) * (G::v_keys * 128) + (r - vp * G::v_keys) * 128 + (c & 7) * 16);
+          };
+          uint32_t(&bd)[4] = bad[nbound % 3];
+          const int r0 = max(0, len - key0), items = (min(TREE_KEYS, (keys - key0 + 15) & ~15) - r0) * CPR;
+          if (ok)
+#pragma unroll 4
+            for (int i = tid; i < items; i += TA_SOFTMAX) {
+              const int r = r0 + i / CPR;
+              uint4* x = word(r, i % CPR);
+              if (key0 + r >= keys) {
+                *x = make_uint4(0, 0, 0, 0);
+              } else {
+                const uint4 y = *x;
+                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                bool odd = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  odd |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+                if (odd) atomicOr(&bd[r >> 5], 1u << (r & 31));
+              }
+            }
+          softmax_barrier();
+          const uint32_t odd4[4] = {bd[0], bd[1], bd[2], bd[3]};
+          if (odd4[0] | odd4[1] | odd4[2] | odd4[3]) {
+            if (ok)
+              for (int i = tid; i < items; i += TA_SOFTMAX) {
+                const int r = r0 + i / CPR;
+                if ((odd4[r >> 5] >> (r & 31)) & 1u) *word(r, i % CPR) = make_uint4(0, 0, 0, 0);
+              }
+            if ((vis[0] & odd4[2 * hh]) | (vis[1] & odd4[2 * hh + 1])) spoilt = true;
+          }
+          fence_proxy_async_smem();
+          if (tid < 4) bad[(nbound + 2) % 3][tid] = 0;
+          ++nbound;
         }
         tc_fence_before();
         __syncwarp();
@@ -374,8 +437,10 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         const bool mine = row < Rv && ok;
         const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) + bad_v : 1.f;
         __nv_bfloat16* orow = a.o + (static_cast<size_t>(it.b) * a.N + tok) * a.Hq * DH + static_cast<size_t>(hq) * DH;
-        const int slot = 2 * blockIdx.x + (it.first ? 0 : 1);
-        float* xrow = whole ? nullptr : a.scratch + (static_cast<size_t>(slot) * min(128, R) + row) * OLD;
+        // a partial segment's rows: [dh / 4][rows][4] floats, then (reference, sum, spoilt) [rows][4], so
+        // that a warp's rows leave side by side
+        const int RW = min(128, R);
+        float* part = a.scratch + static_cast<size_t>(2 * blockIdx.x + (it.tile0 > 0 ? 0 : 1)) * RW * OLD + 4 * row;
 #pragma unroll 1
         for (int c0 = hh * (DH / 2); c0 < (hh + 1) * (DH / 2); c0 += 32) {
           uint32_t ov[32];
@@ -384,22 +449,23 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
           if (!mine) continue;
           if (whole) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t w[4];
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 8; ++i)
                 w[i] = pack_bf16x2(__uint_as_float(ov[e + 2 * i]) * inv, __uint_as_float(ov[e + 2 * i + 1]) * inv);
-              *reinterpret_cast<uint4*>(orow + c0 + e) = make_uint4(w[0], w[1], w[2], w[3]);
+              st_global_32(orow + c0 + e, w);
             }
           } else {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(xrow + c0 + e) = make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+              *reinterpret_cast<uint4*>(part + static_cast<size_t>((c0 + e) / 4) * RW * 4) =
+                  make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
           }
         }
         if (mine && hh == 0) {
           if (!whole) {
-            *reinterpret_cast<float4*>(xrow + DH) = make_float4(ref, lt, bad_v, 0.f);
+            *reinterpret_cast<float4*>(part + static_cast<size_t>(DH / 4) * RW * 4) = make_float4(ref, lt, bad_v, 0.f);
           } else if (a.lse) {
             a.lse[(static_cast<size_t>(it.b) * a.Hq + hq) * a.N + tok] =
                 ref == -INFINITY ? -INFINITY : (ref + log2f(lt)) * 0.6931471805599453f;
@@ -407,7 +473,6 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         }
         tc_fence_before();
       }
-      it.first = 0;
     }
     if (!ok) {
       *abort_v = 1;
@@ -422,46 +487,45 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
 }
 
 // ------------------------------------------------------------------ merge
-// Joins the segments of units that lie on several CTAs.  `wpr` warps share a row (its segments strided
-// over them), 8 / wpr rows per CTA; grid (row groups, row tiles x KV heads, samples).
-constexpr int TM_WARPS = 8;
+// Joins the segments of units that lie on several CTAs.  A thread has 16 features of a row and every
+// `split`-th segment; grid (row groups, row tiles x KV heads, samples).
+constexpr int TM_THREADS = 256;
 
 template <int DH>
-__global__ void __launch_bounds__(TM_WARPS * 32) k_tree_merge(const __grid_constant__ TreeArgs a, int wpr) {
-  constexpr int OLD = DH + 4, VL = DH / 32;   // features per lane
+__global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant__ TreeArgs a, int split) {
+  constexpr int OLD = DH + 4, FG = DH / 16;   // feature groups
   __shared__ long long sh_T, sh_cum;
-  __shared__ float red[TM_WARPS][DH + 4];
-  const int g = a.Hq / a.Hkv, R = g * a.N, RT = (R + 127) >> 7, U = a.Hkv * RT;
-  const int b = blockIdx.z, u = blockIdx.y, rt = u % RT, hk = u / RT;
+  __shared__ float red[TM_THREADS][17];       // reference, 16 features (one split's threads after the other's)
+  __shared__ float red_l[TM_THREADS], red_x[TM_THREADS];
+  const int g = a.Hq / a.Hkv, R = g * a.N, RT = (R + 127) >> 7, NB = (RT + a.rtg - 1) / a.rtg;
+  const int U = a.Hkv * NB;
+  const int b = blockIdx.z, rt = blockIdx.y % RT, hk = blockIdx.y / RT;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rpc = TM_WARPS / wpr;             // rows per CTA
-  const int Rv = min(128, R - rt * 128);
-  const int row = blockIdx.x * rpc + warp / wpr, sub = warp % wpr;
+  const int rows = TM_THREADS / FG / split;   // rows per CTA, side by side in a warp
+  const int Rv = min(128, R - rt * 128), RW = min(128, R);
+  const int sub = tid / (rows * FG), fg = tid / rows % FG, row = blockIdx.x * rows + tid % rows;
   if (warp == 0) {
-    const long long T = tiles_before(a, U, a.B, nullptr);
+    const long long T = tiles_before(a, U, a.B);
     if (lane == 0) sh_T = T;
   } else if (warp == 1) {
-    const long long c = tiles_before(a, U, b, nullptr);
+    const long long c = tiles_before(a, U, b);
     if (lane == 0) sh_cum = c;
   }
   const int nb = sample_tiles(a, b);
   __syncthreads();
   grid_dep_wait();
-  if (nb == 0 || blockIdx.x * rpc >= Rv) return;
-  const long long T = sh_T, t0 = sh_cum + static_cast<long long>(u) * nb, t1 = t0 + nb;
-  // CTA c < n holds tiles [T c / n, T (c + 1) / n), at least one
-  const int n = static_cast<int>(min(T, static_cast<long long>(a.ctas)));
-  auto holder = [&](long long t) { return static_cast<int>(((t + 1) * n - 1) / T); };
-  const int c0 = holder(t0), c1 = holder(t1 - 1);
+  if (nb == 0 || blockIdx.x * rows >= Rv) return;
+  const long long T = sh_T, t0 = sh_cum + static_cast<long long>(hk * NB + rt / a.rtg) * nb;
+  // group c < n holds tiles [T c / n, T (c + 1) / n), at least one
+  const int n = static_cast<int>(min(T, static_cast<long long>(a.groups)));
+  auto holder = [&](long long t) { return static_cast<int>(div_long((t + 1) * n - 1, T)); };
+  const int c0 = holder(t0), c1 = holder(t0 + nb - 1);
   if (c0 == c1) return;   // one segment: written by k_tree_attn
-  // CTA c0's segment of this unit is its first one only if its range begins with it
-  auto part = [&](int c) {
-    const int s = 2 * c + (c == c0 && T * c / n != t0 ? 1 : 0);
-    return a.scratch + (static_cast<size_t>(s) * min(128, R) + row) * OLD;
-  };
-  float m = -INFINITY, l = 0.f, x = 0.f, o[VL];
+  // a CTA's rows that begin a unit are in its second slot, those that go on with one in its first
+  auto slot_of = [&](int c) { return 2 * (c * a.rtg + rt % a.rtg) + (c == c0 ? 1 : 0); };
+  float m = -INFINITY, l = 0.f, x = 0.f, o[16];
 #pragma unroll
-  for (int e = 0; e < VL; ++e) o[e] = 0.f;
+  for (int e = 0; e < 16; ++e) o[e] = 0.f;
   auto add = [&](float m2, float l2, float x2, const float* v) {
     const float mn = fmaxf(m, m2);
     if (mn == -INFINITY) return;
@@ -470,57 +534,59 @@ __global__ void __launch_bounds__(TM_WARPS * 32) k_tree_merge(const __grid_const
     l = l * w0 + l2 * w1;
     x += x2;
 #pragma unroll
-    for (int e = 0; e < VL; ++e) o[e] = o[e] * w0 + v[e] * w1;
+    for (int e = 0; e < 16; ++e) o[e] = o[e] * w0 + v[e] * w1;
   };
   if (row < Rv) {
-    constexpr int UN = 4;   // segments in flight
-    for (int cb = c0 + sub; cb <= c1; cb += UN * wpr) {
-      float v[UN][VL];
-      float4 st[UN];
+    constexpr int UN = 2;   // segments in flight
+    for (int cb = c0 + sub; cb <= c1; cb += UN * split) {
+      float4 v[UN][4], st[UN];
 #pragma unroll
       for (int i = 0; i < UN; ++i) {
-        const int c = cb + i * wpr;
-        st[i] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        const int c = cb + i * split;
         if (c <= c1) {
-          const float* p = part(c);
-          st[i] = *reinterpret_cast<const float4*>(p + DH);
+          const float* p = a.scratch + static_cast<size_t>(slot_of(c)) * RW * OLD + 4 * row;
+          st[i] = *reinterpret_cast<const float4*>(p + static_cast<size_t>(DH / 4) * RW * 4);
 #pragma unroll
-          for (int e = 0; e < VL; e += 2)
-            *reinterpret_cast<float2*>(&v[i][e]) = *reinterpret_cast<const float2*>(p + (e / 2) * 64 + 2 * lane);
+          for (int e = 0; e < 4; ++e) v[i][e] = *reinterpret_cast<const float4*>(p + static_cast<size_t>(fg * 4 + e) * RW * 4);
         }
       }
 #pragma unroll
       for (int i = 0; i < UN; ++i)
-        if (cb + i * wpr <= c1) add(st[i].x, st[i].y, st[i].z, v[i]);
+        if (cb + i * split <= c1) add(st[i].x, st[i].y, st[i].z, reinterpret_cast<const float*>(v[i]));
     }
   }
-  if (wpr > 1) {
+  if (split > 1) {
+    red[tid][0] = m;
 #pragma unroll
-    for (int e = 0; e < VL; e += 2) *reinterpret_cast<float2*>(&red[warp][(e / 2) * 64 + 2 * lane]) = make_float2(o[e], o[e + 1]);
-    if (lane == 0) {
-      red[warp][DH] = m;
-      red[warp][DH + 1] = l;
-      red[warp][DH + 2] = x;
-    }
+    for (int e = 0; e < 16; ++e) red[tid][e + 1] = o[e];
+    red_l[tid] = l;
+    red_x[tid] = x;
     __syncthreads();
     if (sub == 0)
-      for (int w = warp + 1; w < warp + wpr; ++w) {
-        float v[VL];
-#pragma unroll
-        for (int e = 0; e < VL; e += 2) *reinterpret_cast<float2*>(&v[e]) = *reinterpret_cast<float2*>(&red[w][(e / 2) * 64 + 2 * lane]);
-        add(red[w][DH], red[w][DH + 1], red[w][DH + 2], v);
-      }
+      for (int w = tid + rows * FG; w < TM_THREADS; w += rows * FG) add(red[w][0], red_l[w], red_x[w], &red[w][1]);
   }
   if (row >= Rv || sub != 0) return;
   const int rr = rt * 128 + row, tok = rr % a.N, hq = hk * g + rr / a.N;
   const float inv = (l == 0.f ? 0.f : 1.f / l) + x;
-  __nv_bfloat16* orow = a.o + (static_cast<size_t>(b) * a.N + tok) * a.Hq * DH + static_cast<size_t>(hq) * DH;
+  uint32_t w[8];
 #pragma unroll
-  for (int e = 0; e < VL; e += 2)
-    *reinterpret_cast<uint32_t*>(orow + (e / 2) * 64 + 2 * lane) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-  if (a.lse && lane == 0)
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+  st_global_32(a.o + (static_cast<size_t>(b) * a.N + tok) * a.Hq * DH + static_cast<size_t>(hq) * DH + fg * 16, w);
+  if (a.lse && fg == 0)
     a.lse[(static_cast<size_t>(b) * a.Hq + hq) * a.N + tok] =
         m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// CTAs per group: all of a unit's row tiles up to 16; of more, the batch size from 8 to 16 that leaves the
+// fewest CTAs and row tiles of the last batch idle.
+void tree_groups(int ctas, int RT, int& rtg, int& groups) {
+  rtg = std::min(RT, 16);
+  if (RT > 16) {
+    auto busy = [&](int r) { return (ctas / r * r) * static_cast<double>(RT) / ((RT + r - 1) / r * r); };
+    for (int r = 15; r >= 8; --r)
+      if (busy(r) > busy(rtg)) rtg = r;
+  }
+  groups = ctas / rtg;
 }
 
 template <int DH>
@@ -532,24 +598,24 @@ cudaError_t launch_tree(TreeArgs& a, cudaStream_t s) {
       !encode_rows_map(&a.tm_k, a.k, DH, a.S_max, a.S_max, planes, TREE_KEYS, G::k_blocks) ||
       !encode_rows_map(&a.tm_v, a.v, DH, a.S_max, a.S_max, planes, G::v_keys, DH / 64))
     return cudaErrorInvalidValue;
-  k_tree_attn<DH><<<a.ctas, TA_THREADS, G::smem, s>>>(a);
+  k_tree_attn<DH><<<a.groups * a.rtg, TA_THREADS, G::smem, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.S_max <= TREE_KEYS) return e;   // a unit of one tile is never split
   // segments per unit if every sample is as long as can be
-  const int64_t units = static_cast<int64_t>(planes) * RT;
-  const int per = static_cast<int>(a.ctas / std::min<int64_t>(units, a.ctas)) + 1;
-  const int wpr = per > 32 ? 8 : per > 16 ? 4 : per > 8 ? 2 : 1;
-  const int rpc = TM_WARPS / wpr;
+  const int64_t units = static_cast<int64_t>(planes) * ((RT + a.rtg - 1) / a.rtg);
+  const int per = static_cast<int>(a.groups / std::min<int64_t>(units, a.groups)) + 1;
+  const int split = per > 32 ? 8 : per > 16 ? 4 : per > 8 ? 2 : 1;
+  const int rows = TM_THREADS / (DH / 16) / split;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((std::min(R, 128) + rpc - 1) / rpc, a.Hkv * RT, a.B);
-  cfg.blockDim = dim3(TM_WARPS * 32);
+  cfg.gridDim = dim3((std::min(R, 128) + rows - 1) / rows, a.Hkv * RT, a.B);
+  cfg.blockDim = dim3(TM_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_tree_merge<DH>, a, wpr);
+  return cudaLaunchKernelEx(&cfg, k_tree_merge<DH>, a, split);
 }
 
 template <int DH>
@@ -570,7 +636,7 @@ cudaError_t launch_tree_attention(const TreeArgs& args, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  a.ctas = std::min(nsm, TA_CTAS);
+  tree_groups(std::min(nsm, TA_CTAS), (a.Hq / a.Hkv * a.N + 127) / 128, a.rtg, a.groups);
   return a.dh == 64 ? launch_tree<64>(a, s) : a.dh == 128 ? launch_tree<128>(a, s) : launch_tree<256>(a, s);
 }
 

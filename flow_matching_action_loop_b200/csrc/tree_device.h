@@ -19,101 +19,137 @@ __device__ __forceinline__ void report_sample(unsigned* status, uint32_t where, 
   }
 }
 
-// Key tiles of one (sample, KV head): 0 for a padded sample and for one whose length is out of range.
-__device__ __forceinline__ int sample_tiles(const TreeArgs& a, int b) {
-  const int len = a.lens[b];
+// The line of tiles: the samples' units one after the other, a unit's tiles in a row.  A unit is a KV head
+// and a batch of up to a.rtg row tiles (the weights kernel: all rows).  The line is cut into equal ranges,
+// one per group of a.rtg CTAs; CTA r of a group runs row tile r of each batch, so that a group reads a key
+// tile from HBM once and from the L2 after that.
+struct TileRange {
+  long long t0, t1, cum;   // this group's tiles; first tile of sample b
+  int b, len;              // sample of t0
+};
+
+__device__ __forceinline__ int tiles_of(const TreeArgs& a, int len) {
   return len < 0 || len > a.S_max - a.N ? 0 : (len + a.N + TREE_KEYS - 1) / TREE_KEYS;
 }
 
-// The line of tiles: the samples' U units each (attention: KV head major, row tile minor; weights: KV
-// heads), a unit's tiles in a row.
-struct TileRange {
-  long long t0, t1, cum;   // this CTA's tiles; first tile of sample b
-  int b;                   // sample of t0
-};
+// Key tiles of one (sample, KV head): 0 for a padded sample and for one whose length is out of range.
+__device__ __forceinline__ int sample_tiles(const TreeArgs& a, int b) { return tiles_of(a, a.lens[b]); }
 
 struct TileIter {
   long long t, t1, cum;
-  int b, nb, U;
-  // segment
-  int len, hk, rt, tile0, tile1, first;
+  int b, len, nb, U;
+  int hk, rt, tile0, tile1;   // segment: tiles [tile0, tile1) of the nb of unit (b, hk), row tile rt
   __device__ __forceinline__ void start(const TreeArgs& a, const TileRange& r, int U_) {
     t = r.t0;
     t1 = r.t1;
     cum = r.cum;
     b = r.b;
+    len = r.len;
     U = U_;
-    first = 1;
-    nb = t < t1 ? sample_tiles(a, b) : 0;
+    nb = tiles_of(a, len);
   }
-  __device__ __forceinline__ bool next(const TreeArgs& a, int RT) {
-    if (t >= t1) return false;
-    while (t - cum >= static_cast<long long>(U) * nb) {
-      cum += static_cast<long long>(U) * nb;
-      nb = sample_tiles(a, ++b);
-    }
-    const int rel = static_cast<int>(t - cum), u = rel / nb;
-    len = a.lens[b];
-    hk = u / RT;
-    rt = u - hk * RT;
-    tile0 = rel - u * nb;
-    tile1 = static_cast<int>(min(static_cast<long long>(nb), tile0 + (t1 - t)));
-    t += tile1 - tile0;
+  // The next segment, of CTA r of a group whose units have NB batches of the RT row tiles.
+  __device__ __forceinline__ bool next(const TreeArgs& a, int RT, int NB, int r) {
+    do {
+      if (t >= t1) return false;
+      while (t - cum >= static_cast<long long>(U) * nb) {
+        cum += static_cast<long long>(U) * nb;
+        len = a.lens[++b];
+        nb = tiles_of(a, len);
+      }
+      const int rel = static_cast<int>(t - cum), u = rel / nb;
+      hk = NB == 1 ? u : u / NB;
+      rt = (u - hk * NB) * a.rtg + r;
+      tile0 = rel - u * nb;
+      tile1 = static_cast<int>(min(static_cast<long long>(nb), tile0 + (t1 - t)));
+      t += tile1 - tile0;
+    } while (rt >= RT);   // the last batch has fewer row tiles
     return true;
   }
 };
 
-// One warp: the tiles of the samples before b_end; with `status`, samples of a bad length are reported.
-__device__ __forceinline__ long long tiles_before(const TreeArgs& a, int U, int b_end, unsigned* status) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ unsigned long long div_long(unsigned long long x, unsigned long long y) {
+  return (x | y) >> 32 ? x / y : static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+}
+// First tile of CTA c of n: floor(T c / n).
+__device__ __forceinline__ long long share_begin(long long T, int c, int n) {
+  const long long q = div_long(T, n);
+  return q * c + static_cast<int>(T - q * n) * c / n;
+}
+
+// One warp: the tiles of the samples before b_end.
+__device__ __forceinline__ long long tiles_before(const TreeArgs& a, int U, int b_end) {
   long long sum = 0;
-  for (int b0 = 0; b0 < b_end; b0 += 32) {
-    const int b = b0 + lane;
-    int n = 0;
-    if (b < b_end) {
-      n = sample_tiles(a, b);
-      if (status && n == 0 && a.lens[b] >= 0) report_sample(status, CACHE_BAD_LEN, b);
-    }
-    sum += n;
-  }
+  for (int b = threadIdx.x & 31; b < b_end; b += 32) sum += sample_tiles(a, b);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum * U;
 }
 
-// One warp: the sample that holds tile `at`, and the tiles before it.
-__device__ __forceinline__ void find_tile(const TreeArgs& a, int U, long long at, int& b_at, long long& cum_at) {
+// One warp: group c's share of the line.  The first min(T, groups) groups have at least one tile each.
+// CTA 0 reports the samples of a bad length.
+__device__ __forceinline__ TileRange tile_range(const TreeArgs& a, int U, int c) {
   const int lane = threadIdx.x & 31;
-  long long cum = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const long long n = b0 + lane < a.B ? static_cast<long long>(sample_tiles(a, b0 + lane)) * U : 0;
-    long long incl = n;
+  long long T = 0;
+  for (int b = lane; b < a.B; b += 32) {
+    const int len = a.lens[b], n = tiles_of(a, len);
+    if (blockIdx.x == 0 && n == 0 && len >= 0) report_sample(a.status, CACHE_BAD_LEN, b);
+    T += n;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
+  T *= U;
+  const int n = static_cast<int>(min(T, static_cast<long long>(a.groups)));
+  TileRange r = {0, 0, 0, 0, -1};
+  if (c >= n) return r;
+  r.t0 = share_begin(T, c, n);
+  r.t1 = share_begin(T, c + 1, n);
+  for (int b0 = 0; b0 < a.B; b0 += 32) {   // the sample that holds t0
+    const int len = b0 + lane < a.B ? a.lens[b0 + lane] : -1;
+    const long long own = static_cast<long long>(tiles_of(a, len)) * U;
+    long long incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, cum + incl > at);
+    const unsigned hit = __ballot_sync(0xffffffffu, r.cum + incl > r.t0);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      b_at = b0 + l;
-      cum_at = cum + __shfl_sync(0xffffffffu, incl - n, l);
-      return;
+      r.b = b0 + l;
+      r.cum += __shfl_sync(0xffffffffu, incl - own, l);
+      r.len = __shfl_sync(0xffffffffu, len, l);
+      break;
     }
-    cum += __shfl_sync(0xffffffffu, incl, 31);
+    r.cum += __shfl_sync(0xffffffffu, incl, 31);
   }
+  return r;
 }
 
-// One warp: this CTA's share of the line.  The first min(T, CTAs) CTAs have at least one tile each.
-__device__ __forceinline__ TileRange tile_range(const TreeArgs& a, int U) {
-  const long long T = tiles_before(a, U, a.B, blockIdx.x == 0 ? a.status : nullptr);
-  const long long n = min(T, static_cast<long long>(gridDim.x)), c = blockIdx.x;
-  TileRange r;
-  r.t0 = c < n ? T * c / n : 0;
-  r.t1 = c < n ? T * (c + 1) / n : 0;
-  r.b = 0;
-  r.cum = 0;
-  if (r.t0 < r.t1) find_tile(a, U, r.t0, r.b, r.cum);
+// Two float32 operations per instruction (sm_100), each rounded to nearest.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 

@@ -508,7 +508,7 @@ int fr_attention_noalloc(const void* q, const void* k, const void* v, void* o, i
  *     stay as they were, and the fault is latched for fr_ops_sync_status (FR_ERR_DEVICE, the message
  *     gives the where-code 0xc0.. and the sample).
  *   - They run on the current device, on `stream`; every pointer must be memory of that device (checked).
- *     Tensors of 16-byte rows (q, k, v, o) must be 16-byte aligned, the others 4-byte aligned; outputs
+ *     q, k, v and scratch must be 16-byte aligned, o 32-byte, the others 4-byte aligned; outputs
  *     must not overlap inputs.  They allocate nothing and can be captured into graphs (make a first call
  *     on the device before the capture: it sets kernel attributes); two calls that can overlap in time
  *     need scratch buffers of their own.  Results do not depend on the launch (no float

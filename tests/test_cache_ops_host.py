@@ -65,9 +65,9 @@ def test_attention_pointers_refused(abi):
             args = [A] * 7
             args[i] = bad
             assert lib.fr_attention_weights(*args, *sizes, None) == abi.FR_ERR_ARG
-    for i in (4, 6):
+    for i, bad in ((4, A + 1), (6, A + 1), (5, A + 16), (0, A + 8)):   # o is stored 32 bytes at a time
         args = [A] * 7
-        args[i] = A + 1
+        args[i] = bad
         assert lib.fr_attention_tree(*args, *sizes, A, 1 << 30, None) == abi.FR_ERR_ARG
 
 
