@@ -292,7 +292,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
     const uint32_t lanes = static_cast<uint32_t>(pw * 32) << 16;
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in log2 units
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, WAIT_LIMIT_NS) && !*abort_v);
+      if (!__all_sync(0xffffffffu, mbar_test(bar, parity)) && ok)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, WAIT_LIMIT_NS) && !*abort_v);
       tc_fence_after();
     };
     int t = 0, nbound = 0;
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
             ps[(e >> 1) & 1] = add_f32x2(ps[(e >> 1) & 1], pack_f32x2(p0, p1));
             pk[e >> 1] = pack_bf16x2(p0, p1);
           }
-          if (t >= 2) wait(&bar_o[t & 1], ((t - 2) >> 1) & 1);   // P(t - 2) has been read
+          // P(t - 2) has been read: its product was issued before S(t), whose commit covers it
           tmem_st32(tP + (t & 1) * 64 + lanes + 32 * hh, pk);
           const float2 pt = unpack_f32x2(add_f32x2(ps[0], ps[1]));
           l = l * corr + (pt.x + pt.y);
