@@ -10,16 +10,19 @@
 // 2.6 times at 6 x 33000 slots and four row tiles).
 //
 // Inside a CTA, per tile t:
-//   copy warp     K(t+1), V(t) by tensor map (128-byte swizzle) into a ring of shared-memory slots
-//   MMA warp      S(t+1) = Q K(t+1)^T, then O += P(t) V(t): tcgen05, fp32 in tensor memory; P is the A
-//                 operand from tensor memory
-//   softmax warps (8) two threads per row, 64 slots each: running maximum and sum in fp32, P = 2^(s - ref)
-// The scores leave their columns for registers at the start of a tile's softmax, so the tensor core works on
-// P(t-1) V(t-1) and S(t+1) while the softmax of tile t runs: it waits for neither the other's end (with P
-// in the columns of the scores, S(t+1) waited for P(t-1) V(t-1): 1.97 us a tile at dh = 256 instead of
-// the 1.54 us of the products).  The reference
-// of a row's exponentials moves only when its maximum has grown by more than 2^8 (P stays below 2^8, O and
-// the sum keep one reference, O / sum is unchanged): O is rescaled rarely.
+//   copy warp     K(t+LA), V(t) by tensor map (128-byte swizzle) into a ring of shared-memory slots
+//   MMA warp      S(t+LA) = Q K^T, then O += P(t) V(t): tcgen05, fp32 in tensor memory; P is the A operand
+//                 from tensor memory
+//   softmax warps two groups of four take the tiles in turn, a thread a row: maximum and sum in fp32,
+//                 P = 2^(s - ref)
+// One group's loads, maxima and stores thus overlap the other's exponentials (with both groups on one tile,
+// half a row each, the multi-function unit idled half of a tile's 2500 cycles).  The groups hand the row's
+// reference on from tile to tile.  Two score buffers (LA = 2) let both groups have a tile; at dh = 256
+// tensor memory has room for one (LA = 1), and S(t+1) is issued once the scores of tile t are in registers.
+// P has columns of its own: with P in those of the scores, S(t+1) waited for P(t-1) V(t-1) as well (1.97 us a
+// tile at dh = 256 instead of 1.6).
+// The reference of a row's exponentials moves only when its maximum has grown by more than 2^8 (P stays
+// below 2^8, O and the sum keep one reference, O / sum is unchanged): O is rescaled rarely.
 // P is rounded to bf16, the tensor core's operand type: half a bf16 step per weight, as much as the
 // rounding of o itself.
 #include <algorithm>
@@ -45,7 +48,8 @@ template <int DH>
 struct TreeGeom {
   static constexpr int pieces = DH == 256 ? 2 : 1;              // per K or V tile
   static constexpr int piece = TREE_KEYS * DH * 2 / pieces;     // bytes
-  static constexpr int QB = DH == 256 ? 1 : 2;
+  static constexpr int LA = DH == 256 ? 1 : 2;                  // score buffers, tiles that S runs ahead
+  static constexpr int QB = LA;                                 // query tiles
   static constexpr int NS = DH == 64 ? 10 : 5;
   static constexpr int q_bytes = 128 * DH * 2;
   static constexpr int smem = QB * q_bytes + NS * piece;
@@ -60,24 +64,30 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
                : "memory");
 }
 
+// Named barriers: 1..4 the two warps of a lane quadrant, 5 and 6 a softmax group, 7..14 the reference of
+// (quadrant, group) on its way to the other group.
 __device__ __forceinline__ void pair_barrier(int w) { asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory"); }
-__device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
+__device__ __forceinline__ void group_barrier(int g) { asm volatile("bar.sync %0, 128;" ::"r"(5 + g) : "memory"); }
+__device__ __forceinline__ void ref_send(int w, int g) { asm volatile("bar.arrive %0, 64;" ::"r"(7 + 2 * w + g) : "memory"); }
+__device__ __forceinline__ void ref_wait(int w, int g) { asm volatile("bar.sync %0, 64;" ::"r"(7 + 2 * w + g) : "memory"); }
 
 template <int DH>
 __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_constant__ TreeArgs a) {
   using G = TreeGeom<DH>;
   extern __shared__ __align__(1024) uint8_t dsm[];
-  __shared__ uint64_t full[G::NS], empty[G::NS], q_full[2], q_empty[2], bar_s, bar_l, bar_o[2], bar_p[2], fin_bar;
+  // bar_s, bar_l, bar_p, bar_o [tile parity]: scores written, scores read, P written, O updated.  Each is
+  // waited for by one group (or the MMA warp) in every phase: none is passed on an older phase's parity.
+  __shared__ uint64_t full[G::NS], empty[G::NS], q_full[2], q_empty[2], bar_s[2], bar_l[2], bar_o[2], bar_p[2], fin_bar;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ TileIter first_seg;           // its segment: the first
   __shared__ int any_seg;
-  __shared__ float mx_sh[2][2][128];       // [tile parity][half][row]; a segment's sums at its end
-  __shared__ uint32_t bad[3][4];           // drafted value rows of a tile that are not finite
+  __shared__ float ref_sh[2][128], sum_sh[2][128];   // of the groups' last tiles
+  __shared__ uint32_t bad[2][3][4];        // [group]: drafted value rows of a tile that are not finite
   constexpr uint32_t IDESC_S = idesc_f32acc(FMT_BF16, 128, TREE_KEYS);
   constexpr uint32_t IDESC_O = idesc_f32acc(FMT_BF16, 128, DH) | IDESC_B_MN_MAJOR;
   constexpr int OLD = DH + 4;              // floats per partial row: O, reference, sum, NaN if spoilt
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = a.Hq / a.Hkv, R = g * a.N, RT = (R + 127) >> 7, NB = (RT + a.rtg - 1) / a.rtg;
   const int grp = blockIdx.x / a.rtg, r_in = blockIdx.x - grp * a.rtg;
   uint8_t* ring = dsm + G::QB * G::q_bytes;
@@ -119,10 +129,10 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         mbar_init(&q_full[i], 1);
         mbar_init(&q_empty[i], 1);
         mbar_init(&bar_o[i], 1);
-        mbar_init(&bar_p[i], TA_SOFTMAX / 32);
+        mbar_init(&bar_p[i], 4);
+        mbar_init(&bar_s[i], 1);
+        mbar_init(&bar_l[i], 4);
       }
-      mbar_init(&bar_s, 1);
-      mbar_init(&bar_l, TA_SOFTMAX / 32);
       mbar_init(&fin_bar, 1);
       abort_flag = 0;
       fence_mbar_init();
@@ -140,7 +150,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
       first_seg = it;
     }
   }
-  if (tid < 12) bad[tid >> 2][tid & 3] = 0;
+  if (tid < 24) (&bad[0][0][0])[tid] = 0;
   if (warp == 0) {
     tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
@@ -149,146 +159,149 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // tensor memory: scores (128 columns), two P tiles (64 each), O (dh)
-  const uint32_t tS = tmem_base, tP = tmem_base + 128, tO = tmem_base + 256;
+  // tensor memory: LA score buffers (128 columns each), two P tiles (64 each), O (dh)
+  const uint32_t tS = __shfl_sync(0xffffffffu, tmem_base, 0), tP = tS + 128 * G::LA, tO = tP + 128;
   TileIter it = first_seg;
   bool more = any_seg != 0;
 
   if (warp == TA_SOFTMAX / 32) {
-    // ---------------- copies: pieces in the order the MMA warp takes them, K(0), then K(t+1), V(t)
+    // ---------------- copies: pieces in the order the MMA warp takes them, K(0) .. K(LA-1), then K(t+LA), V(t).
+    // The places of K tiles past the last are left out, so that V(t) is always at pieces * (2 t + LA + 1).
     if ((tid & 31) == 0 && more) {
-      int tile = it.tile0;   // K(t) has been issued
-      for (;;) {
-        const int v_plane = it.b * a.Hkv + it.hk, v_key = tile * TREE_KEYS;
-        if (++tile == it.tile1) {
+      TileIter vi = it;
+      int tile = it.tile0, nk = 1;   // K side: K(nk - 1) has been issued
+      auto next_k = [&]() {
+        if (more && ++tile == it.tile1) {
           more = it.next(a, RT, NB, r_in);
           tile = it.tile0;
-          if (more) ok = load_q(it);
+          if (more && !load_q(it)) return false;
         }
-        if (more) ok = ok && load_k(it, tile);
-        else pos += G::pieces;   // V(t) is at position pieces * (2 t + 2) for the last tile too
-        for (int p = 0; ok && p < G::pieces; ++p) ok = load_piece(&a.tm_v, v_key + p * G::v_keys, 0, v_plane);
-        if (!ok || !more) break;
+        if (!more) {
+          pos += G::pieces;
+          return true;
+        }
+        ++nk;
+        return load_k(it, tile);
+      };
+      if (G::LA == 2) ok = next_k();
+      bool more_v = true;
+      for (int vt = vi.tile0; ok && more_v;) {
+        ok = next_k();
+        const int plane = vi.b * a.Hkv + vi.hk;
+        for (int p = 0; ok && p < G::pieces; ++p) ok = load_piece(&a.tm_v, vt * TREE_KEYS + p * G::v_keys, 0, plane);
+        if (++vt == vi.tile1) {
+          more_v = vi.next(a, RT, NB, r_in);
+          vt = vi.tile0;
+        }
       }
       if (!ok) {
         *abort_v = 1;
         report_timeout(a.status, 0x710);
       }
-      // no copy is in flight when the CTA leaves (a position that was left out waits for the slot's last use)
+      // no copy is in flight when the CTA leaves
       for (int p = max(0, pos - G::NS); p < pos; ++p) {
-        const bool skipped = !more && p >= pos - 2 * G::pieces && p < pos - G::pieces && ok;
-        if (!skipped) mbar_wait(&full[p % G::NS], (p / G::NS) & 1, WAIT_LIMIT_NS);
+        const int i = p / G::pieces - G::LA;
+        if (i >= 0 ? i % 2 != 0 || i / 2 + G::LA < nk : i + G::LA < nk)   // not a place left out
+          mbar_wait(&full[p % G::NS], (p / G::NS) & 1, WAIT_LIMIT_NS);
       }
       for (int s = max(0, seg - G::QB + 1); s <= seg; ++s)
         mbar_wait(&q_full[s % G::QB], (s / G::QB) & 1, WAIT_LIMIT_NS);
     }
   } else if (warp == TA_SOFTMAX / 32 + 1) {
-    // ---------------- MMAs
-    if ((tid & 31) == 0 && more) {
-      // The products of S(t+1) and of P(t) V(t) alternate.  What the next ones wait for is tested before the
-      // last of the present ones are issued, so that no barrier's latency lies between them.
-      int mpos = 0, mseg = -1, tile = it.tile0;   // ring position; S side: segment, tile of segment `it`
-      auto landed = [&](int p) { return mbar_test(&full[(mpos + p) % G::NS], ((mpos + p) / G::NS) & 1); };
-      auto wait_pieces = [&]() {
-        for (int p = 0; p < G::pieces; ++p)
-          if (!mbar_wait(&full[(mpos + p) % G::NS], ((mpos + p) / G::NS) & 1, WAIT_LIMIT_NS)) return false;
-        return !*abort_v;
-      };
-      bool more_s = true, s_begins = true;
-      auto advance_s = [&]() {   // the next tile of the S side
-        s_begins = false;
-        if (++tile == it.tile1) {
-          more_s = it.next(a, RT, NB, r_in);
-          tile = it.tile0;
-          s_begins = true;
-        }
-      };
-      auto s_wait = [&](int t) {
-        if (s_begins && !mbar_wait(&q_full[(mseg + 1) % G::QB], ((mseg + 1) / G::QB) & 1, WAIT_LIMIT_NS)) return false;
-        if (t > 0 && !mbar_wait(&bar_l, (t - 1) & 1, WAIT_LIMIT_NS)) return false;   // S(t - 1) has been read
-        return wait_pieces();
-      };
-      // Returns whether P(t - 1) and V(t - 1) are there.
-      auto issue_s = [&](int t) {
-        if (s_begins) ++mseg;
-        tc_fence_after();
-        const uint32_t qa = smem_u32(dsm + (mseg % G::QB) * G::q_bytes);
-        bool r = false;
+    // ---------------- MMAs, the whole warp in step
+    if (more) {
+      // S runs up to LA tiles ahead of P V.  Whichever has what it waits for is issued next, S first (a
+      // softmax group may wait for it); in a fixed order S(t+LA) waited for the softmax of tile t-1.
+      // A barrier is tested only where its phase before is known to have completed.
+      const bool leader = elect_one();
+      auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };   // known to be uniform
+      TileIter vi = it;
+      int ts = 0, tv = 0, seg_s = 0;                        // next S and P V, query tile
+      int st = same(it.tile1 - it.tile0), vt = st;          // tiles left of their segments
+      bool more_s = true, s_begins = true, v_begins = true; // a segment begins with the tile
+      auto test = [](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)); };
+      auto landed = [&](int p) {   // a tile's pieces, from ring position p on
+        bool r = true;
 #pragma unroll
-        for (int p = 0; p < G::pieces; ++p) {
-          const uint32_t ka = smem_u32(ring + ((mpos + p) % G::NS) * G::piece);
-#pragma unroll
-          for (int k = 0; k < G::k_blocks * 4; ++k) {
-            if (p == G::pieces - 1 && k == G::k_blocks * 4 - 2 && t > 0) {
-              r = mbar_test(&bar_p[(t - 1) & 1], ((t - 1) >> 1) & 1);
-              for (int i = 0; i < G::pieces; ++i) r &= landed(G::pieces + i);
-            }
-            mma_bf16(tS, smem_desc_sw128(qa + (p * G::k_blocks + (k >> 2)) * (128 * 128) + (k & 3) * 32, 16, 1024),
-                     smem_desc_sw128(ka + (k >> 2) * (TREE_KEYS * 128) + (k & 3) * 32, 16, 1024), IDESC_S,
-                     p > 0 || k > 0);
-          }
-          mma_commit(&empty[(mpos + p) % G::NS]);
-        }
-        mma_commit(&bar_s);
-        if (tile + 1 == it.tile1) mma_commit(&q_empty[mseg % G::QB]);
-        mpos += G::pieces;
+        for (int i = 0; i < G::pieces; ++i) r = r && test(&full[(p + i) % G::NS], (p + i) / G::NS);
         return r;
       };
-      bool v_begins = true, s_ok = false;   // V(t) is a segment's first; S(t + 1) can be issued
-      int keys_v = it.len + a.N - tile * TREE_KEYS;
-      ok = s_wait(0);
-      if (ok) issue_s(0);
-      for (int t = 0; ok; ++t) {
-        advance_s();
-        bool pv_ok = false;
-        const int keys_s = more_s ? it.len + a.N - tile * TREE_KEYS : 0;
-        if (more_s) {
-          ok = s_ok || s_wait(t + 1);
-          if (!ok) break;
-          pv_ok = issue_s(t + 1);
-        } else {
-          mpos += G::pieces;
-        }
-        if (!pv_ok) ok = mbar_wait(&bar_p[t & 1], (t >> 1) & 1, WAIT_LIMIT_NS) && wait_pieces();
-        if (!ok) break;
-        tc_fence_after();
-        const int steps = min(TREE_KEYS, keys_v + 15) / 16;   // of 16 slots: those that hold slots in use
-        s_ok = false;
+      const uint64_t dq = smem_desc_sw128(smem_u32(dsm), 16, 1024), dk = smem_desc_sw128(smem_u32(ring), 16, 1024),
+                     dv = smem_desc_sw128(smem_u32(ring), G::v_keys * 128, 1024);   // + byte offset / 16
+      uint64_t idle = 0;
+      for (;;) {
+        const int pk = G::pieces * (ts < G::LA ? ts : 2 * ts - G::LA), pv = G::pieces * (2 * tv + G::LA + 1);
+        if (more_s && (!s_begins || test(&q_full[seg_s % G::QB], seg_s / G::QB)) &&
+            (ts < G::LA || test(&bar_l[(ts - G::LA) & 1], (ts - G::LA) >> 1)) && landed(pk)) {
+          tc_fence_after();
+          const uint64_t qd = dq + (seg_s % G::QB) * (G::q_bytes / 16);
+          const uint32_t d = tS + (ts % G::LA) * TREE_KEYS;
 #pragma unroll
-        for (int p = 0; p < G::pieces; ++p) {
-          const uint32_t va = smem_u32(ring + ((mpos + p) % G::NS) * G::piece);
+          for (int p = 0; p < G::pieces; ++p) {
+            const uint64_t kd = dk + ((pk + p) % G::NS) * (G::piece / 16);
 #pragma unroll
-          for (int k = 0; k < G::v_keys / 16; ++k) {
-            const int step = p * (G::v_keys / 16) + k;
-            if (step == TREE_KEYS / 16 - 1 && more_s && tile + 1 < it.tile1) {
-              // S(t + 2) follows in the same segment
-              s_ok = mbar_test(&bar_l, (t + 1) & 1);
-              for (int i = 0; i < G::pieces; ++i) s_ok &= landed(G::pieces + i);
-            }
-            if (step < steps)
-              mma_bf16_ta(tO, tP + (t & 1) * 64 + step * 8, smem_desc_sw128(va + k * 2048, G::v_keys * 128, 1024), IDESC_O,
-                          (!v_begins || step > 0) ? 1u : 0u);
+            for (int k = 0; k < G::k_blocks * 4; ++k)
+              mma_bf16_warp(leader, d, qd + ((p * G::k_blocks + (k >> 2)) * (128 * 128) + (k & 3) * 32) / 16,
+                            kd + ((k >> 2) * (TREE_KEYS * 128) + (k & 3) * 32) / 16, IDESC_S, p > 0 || k > 0);
+            mma_commit_warp(leader, &empty[(pk + p) % G::NS]);
           }
-          mma_commit(&empty[(mpos + p) % G::NS]);
+          mma_commit_warp(leader, &bar_s[ts & 1]);
+          ++ts;
+          s_begins = false;
+          if (--st == 0) {
+            mma_commit_warp(leader, &q_empty[seg_s % G::QB]);
+            more_s = same(it.next(a, RT, NB, r_in)) != 0;
+            st = same(it.tile1 - it.tile0);
+            s_begins = true;
+            ++seg_s;
+          }
+        } else if (tv < ts && test(&bar_p[tv & 1], tv >> 1) && landed(pv)) {
+          tc_fence_after();
+          // steps of 16 slots: those that hold slots in use
+          const int steps = same(min(TREE_KEYS, vi.len + a.N - (vi.tile1 - vt) * TREE_KEYS + 15) / 16);
+          const uint32_t p_tm = tP + (tv & 1) * 64;
+#pragma unroll
+          for (int p = 0; p < G::pieces; ++p) {
+            const uint64_t vd = dv + ((pv + p) % G::NS) * (G::piece / 16);
+#pragma unroll
+            for (int k = 0; k < G::v_keys / 16; ++k) {
+              const int step = p * (G::v_keys / 16) + k;
+              if (step < steps)
+                mma_bf16_ta_warp(leader, tO, p_tm + step * 8, vd + k * 128, IDESC_O, (!v_begins || step > 0) ? 1u : 0u);
+            }
+            mma_commit_warp(leader, &empty[(pv + p) % G::NS]);
+          }
+          mma_commit_warp(leader, &bar_o[tv & 1]);
+          ++tv;
+          v_begins = false;
+          if (--vt == 0) {
+            if (same(vi.next(a, RT, NB, r_in)) == 0) break;
+            vt = same(vi.tile1 - vi.tile0);
+            v_begins = true;
+          }
+        } else {
+          const uint64_t now = globaltimer();
+          if (idle == 0) idle = now;
+          if (__any_sync(0xffffffffu, now - idle > WAIT_LIMIT_NS || *abort_v)) {
+            ok = false;
+            break;
+          }
+          continue;
         }
-        mma_commit(&bar_o[t & 1]);
-        mpos += G::pieces;
-        if (!more_s) break;
-        v_begins = s_begins;
-        keys_v = keys_s;
+        idle = 0;
       }
       if (!ok) {
         *abort_v = 1;
-        report_timeout(a.status, 0x711);
+        if (leader) report_timeout(a.status, 0x711);
       }
       // every MMA issued has completed before tensor memory is freed
-      mma_commit(&fin_bar);
-      if (!mbar_wait(&fin_bar, 0, WAIT_LIMIT_NS)) report_timeout(a.status, 0x712);
+      mma_commit_warp(leader, &fin_bar);
+      if (!mbar_wait(&fin_bar, 0, WAIT_LIMIT_NS) && leader) report_timeout(a.status, 0x712);
     }
   } else {
     // ---------------- softmax.  A warp whose wait gave up goes on without waiting (the named barriers
     // need every warp) and stores nothing.
-    const int row = tid & 127, hh = tid >> 7, pw = warp & 3;
+    const int row = tid & 127, hh = tid >> 7, pw = warp & 3;   // row of the tile, group, lane quadrant
     const uint32_t lanes = static_cast<uint32_t>(pw * 32) << 16;
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in log2 units
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -304,48 +317,45 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
       const int tok = rr % a.N, hq = it.hk * g + rr / a.N;
       const uint32_t* words = a.mask ? a.mask + (static_cast<size_t>(it.b) * a.N + min(tok, a.N - 1)) * a.W : nullptr;
       const int len = it.len, keys = len + a.N;
-      float ref = -INFINITY, l = 0.f;
+      float ref = -INFINITY, l = 0.f;                  // of this group's tiles so far
       bool spoilt = false;                             // a drafted value row that this row sees is not finite
       for (int tile = it.tile0; tile < it.tile1; ++tile, ++t) {
+        if ((t & 1) != hh) continue;
         const int key0 = tile * TREE_KEYS;
         const bool boundary = key0 + TREE_KEYS > len;  // holds drafted slots or slots past them
-        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
+        uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (boundary) {
-          const int j0 = key0 + 64 * hh - len;
-          vis[0] = seen_slots(words, tok, a.N, j0);
-          vis[1] = seen_slots(words, tok, a.N, j0 + 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vis[i] = seen_slots(words, tok, a.N, key0 + 32 * i - len);
         }
-        wait(&bar_s, t & 1);
+        wait(&bar_s[t & 1], (t >> 1) & 1);
+        const uint32_t ts = tS + (t % G::LA) * TREE_KEYS + lanes, tp = tP + (t & 1) * 64 + lanes;
+        float corr = 1.f, off = 0.f;
+        const uint64_t sl22 = pack_f32x2(sl2, sl2);
+        uint64_t ps[2] = {0, 0};
         uint32_t s[64];
-        if (work) {
-          tmem_ld32_nowait(tS + lanes + 64 * hh, s);
-          tmem_ld32_nowait(tS + lanes + 64 * hh + 32, s + 32);
+        // half of the row's scores, 64 * half on, hidden ones -inf
+        auto load = [&](int half) {
+          tmem_ld32_nowait(ts + 64 * half, s);
+          tmem_ld32_nowait(ts + 64 * half + 32, s + 32);
           tmem_wait_ld();
-          tc_fence_before();
-        }
-        __syncwarp();
-        if ((tid & 31) == 0) mbar_arrive(&bar_l);
-        if (work) {
           if (boundary) {
 #pragma unroll
             for (int e = 0; e < 64; ++e)
-              if (!((vis[e >> 5] >> (e & 31)) & 1u)) s[e] = 0xff800000u;   // -inf
+              if (!(((half ? vis[2 + (e >> 5)] : vis[e >> 5]) >> (e & 31)) & 1u)) s[e] = 0xff800000u;
           }
+        };
+        auto maximum = [&]() {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
             float& m = m4[(e >> 1) & 3];
             m = max3(m, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
           }
-          const float mine = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          mx_sh[t & 1][hh][row] = mine;
-          pair_barrier(pw);
-          const float mx = fmaxf(mine, mx_sh[t & 1][hh ^ 1][row]) * sl2;
-          const float nref = mx > ref + TA_RESCALE || ref == -INFINITY ? fmaxf(mx, ref) : ref;
-          const float corr = nref == -INFINITY ? 1.f : exp2f(ref - nref);   // first visible slot: 0
-          const float off = nref == -INFINITY ? 0.f : nref;
-          const uint64_t sl22 = pack_f32x2(sl2, sl2), off2 = pack_f32x2(-off, -off);
-          uint64_t ps[2] = {0, 0};
+          return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        };
+        auto weights = [&](int half) {   // P of half a row
+          const uint64_t off2 = pack_f32x2(-off, -off);
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
@@ -355,42 +365,75 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
             ps[(e >> 1) & 1] = add_f32x2(ps[(e >> 1) & 1], pack_f32x2(p0, p1));
             pk[e >> 1] = pack_bf16x2(p0, p1);
           }
-          // P(t - 2) has been read: its product was issued before S(t), whose commit covers it
-          tmem_st32(tP + (t & 1) * 64 + lanes + 32 * hh, pk);
+          tmem_st32(tp + 32 * half, pk);
+        };
+        if (work) {
+          load(0);
+          float mx = maximum();
+          load(1);
+          mx = fmaxf(mx, maximum()) * sl2;
+          // the reference after the tile before this one: the other group's
+          float before = -INFINITY;
+          if (tile > it.tile0) {
+            ref_wait(pw, hh ^ 1);
+            before = ref_sh[hh ^ 1][row];
+          }
+          const float nref = mx > before + TA_RESCALE || before == -INFINITY ? fmaxf(mx, before) : before;
+          if (tile + 1 < it.tile1) {
+            ref_sh[hh][row] = nref;
+            ref_send(pw, hh);
+          }
+          if (nref != -INFINITY) {
+            corr = exp2f(before - nref);   // first visible slot: 0
+            l *= exp2f(ref - nref);
+            off = nref;
+          }
+          ref = nref;
+        }
+        wait(&bar_o[t & 1], ((t >> 1) - 1) & 1);   // P(t - 2) has been read
+        if (work) {
+          weights(1);
+          load(0);
+          tc_fence_before();
+        }
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(&bar_l[t & 1]);
+        if (work) {
+          weights(0);
           const float2 pt = unpack_f32x2(add_f32x2(ps[0], ps[1]));
-          l = l * corr + (pt.x + pt.y);
+          l += pt.x + pt.y;
           if (tile > it.tile0 && __any_sync(0xffffffffu, corr != 1.f)) {
             wait(&bar_o[(t - 1) & 1], ((t - 1) >> 1) & 1);   // O holds the tiles before this one
 #pragma unroll 1
-            for (int c0 = hh * (DH / 2); c0 < (hh + 1) * (DH / 2); c0 += 32) {
-              uint32_t ov[32];
-              tmem_ld32_nowait(tO + lanes + c0, ov);
+            for (int c0 = 0; c0 < DH; c0 += 32) {
+              tmem_ld32_nowait(tO + lanes + c0, s);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
-              tmem_st32(tO + lanes + c0, ov);
+              for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * corr);
+              tmem_st32(tO + lanes + c0, s);
             }
           }
-          ref = nref;
           tmem_wait_st();
         }
         if (boundary) {
           // Values that a row does not see must not reach it through 0 * NaN: drafted rows that are not
           // finite, and the rows past the drafts in the last step of 16 slots that the product takes, are
           // zeroed where they landed.
-          const int pv = G::pieces * (2 * t + 2);            // ring position of V(t)
+          const int pv = G::pieces * (2 * t + G::LA + 1);    // ring position of V(t)
+          // (a slot's phase can be told only once its use before is known to have landed: it was V(t - 1)'s at most)
+          if (t > 0) wait(&bar_o[(t - 1) & 1], ((t - 1) >> 1) & 1);
           for (int p = 0; p < G::pieces; ++p) wait(&full[(pv + p) % G::NS], ((pv + p) / G::NS) & 1);
           constexpr int CPR = DH / 8;                        // 16-byte words per row
           auto word = [&](int r, int c) {
             const int vp = r / G::v_keys;
-            return reinterpret_cast<uint4*>(ring + ((pv + vp) % G::NS) * G::piece +
-                                            (c >> 3) * (G::v_keys * 128) + (r - vp * G::v_keys) * 128 + (c & 7) * 16);
+            return reinterpret_cast<uint4*>(ring + ((pv + vp) % G::NS) * G::piece + (c >> 3) * (G::v_keys * 128) +
+                                            (r - vp * G::v_keys) * 128 + (c & 7) * 16);
           };
-          uint32_t(&bd)[4] = bad[nbound % 3];
+          uint32_t(&bd)[4] = bad[hh][nbound % 3];
           const int r0 = max(0, len - key0), items = (min(TREE_KEYS, (keys - key0 + 15) & ~15) - r0) * CPR;
           if (ok)
 #pragma unroll 4
-            for (int i = tid; i < items; i += TA_SOFTMAX) {
+            for (int i = row; i < items; i += 128) {
               const int r = r0 + i / CPR;
               uint4* x = word(r, i % CPR);
               if (key0 + r >= keys) {
@@ -405,18 +448,21 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
                 if (odd) atomicOr(&bd[r >> 5], 1u << (r & 31));
               }
             }
-          softmax_barrier();
-          const uint32_t odd4[4] = {bd[0], bd[1], bd[2], bd[3]};
+          group_barrier(hh);
+          uint32_t odd4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) odd4[i] = bd[i];
           if (odd4[0] | odd4[1] | odd4[2] | odd4[3]) {
             if (ok)
-              for (int i = tid; i < items; i += TA_SOFTMAX) {
+              for (int i = row; i < items; i += 128) {
                 const int r = r0 + i / CPR;
-                if ((odd4[r >> 5] >> (r & 31)) & 1u) *word(r, i % CPR) = make_uint4(0, 0, 0, 0);
+                if ((bd[r >> 5] >> (r & 31)) & 1u) *word(r, i % CPR) = make_uint4(0, 0, 0, 0);
               }
-            if ((vis[0] & odd4[2 * hh]) | (vis[1] & odd4[2 * hh + 1])) spoilt = true;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) spoilt |= (vis[i] & odd4[i]) != 0;
           }
           fence_proxy_async_smem();
-          if (tid < 4) bad[(nbound + 2) % 3][tid] = 0;
+          if (row < 4) bad[hh][(nbound + 2) % 3][row] = 0;
           ++nbound;
         }
         tc_fence_before();
@@ -425,14 +471,15 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
       }
       // ---------------- the segment's rows
       wait(&bar_o[(t - 1) & 1], ((t - 1) >> 1) & 1);
-      if (work) {
-        // the halves' sums; the sign says that a value row was not finite
-        float(&sums)[2][128] = mx_sh[t & 1];   // last read before this tile's barrier
-        sums[hh][row] = spoilt ? -l : l;
+      {
+        // the groups' sums, brought to the last tile's reference; the sign says that a value row was not finite
+        sum_sh[hh][row] = spoilt ? -l : l;
+        ref_sh[hh][row] = ref;
         pair_barrier(pw);
-        const float l0 = sums[0][row], l1 = sums[1][row];
-        pair_barrier(pw);                      // before the next tile's maxima
-        const float lt = fabsf(l0) + fabsf(l1);
+        const float l0 = sum_sh[0][row], l1 = sum_sh[1][row], r0 = ref_sh[0][row], r1 = ref_sh[1][row];
+        ref = fmaxf(r0, r1);
+        const float at = ref == -INFINITY ? 0.f : ref;
+        const float lt = fabsf(l0) * exp2f(r0 - at) + fabsf(l1) * exp2f(r1 - at);
         const float bad_v = signbit(l0) || signbit(l1) ? NAN : 0.f;
         const bool whole = it.tile1 - it.tile0 == it.nb;
         const bool mine = row < Rv && ok;
@@ -447,7 +494,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
           uint32_t ov[32];
           tmem_ld32_nowait(tO + lanes + c0, ov);
           tmem_wait_ld();
-          if (!mine) continue;
+          if (!mine || !work) continue;
           if (whole) {
 #pragma unroll
             for (int e = 0; e < 32; e += 16) {
@@ -473,6 +520,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
           }
         }
         tc_fence_before();
+        pair_barrier(pw);   // both groups have read O and the sums before either goes on
       }
     }
     if (!ok) {

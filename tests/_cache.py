@@ -21,20 +21,6 @@ def words_of(seen):
     return out
 
 
-def attend_row(q, k, v, visible):
-    """One row: (o, lse, sum of p|v|, largest sum |q_d k_d| / sqrt(dh)) over the visible slots."""
-    dh = len(q)
-    idx = np.flatnonzero(visible)
-    if len(idx) == 0:
-        return np.zeros(dh), -np.inf, np.zeros(dh), 0.0
-    kk, vv = k[idx], v[idx]
-    s = kk @ q / np.sqrt(dh)
-    m = s.max()
-    e = np.exp(s - m)
-    p = e / e.sum()
-    return p @ vv, m + np.log(e.sum()), p @ np.abs(vv), float((np.abs(kk) @ np.abs(q)).max() / np.sqrt(dh))
-
-
 def attend(q, k, v, lens, words):
     """q [B][Hq][N][dh], k, v [B][Hkv][S][dh]: o, its tolerance's sums, lse and score sizes; padded samples stay 0."""
     B, Hq, N, dh = q.shape
@@ -45,11 +31,19 @@ def attend(q, k, v, lens, words):
         if n0 < 0:
             continue
         seen = sees(None if words is None else words[b], N)
-        for i in range(N):
-            vis = np.concatenate([np.ones(n0, bool), seen[i]])
-            for h in range(Hq):
-                o[b, i, h], lse[b, h, i], pv[b, i, h], size[b, h, i] = attend_row(
-                    q[b, h, i], k[b, h // g, :n0 + N], v[b, h // g, :n0 + N], vis)
+        for h in range(Hq):
+            kk, vv = k[b, h // g, :n0 + N], v[b, h // g, :n0 + N]
+            vis = np.concatenate([np.ones((N, n0), bool), seen], axis=1)
+            s = np.where(vis, q[b, h] @ kk.T / np.sqrt(dh), -np.inf)
+            m = s.max(axis=1)
+            some = m > -np.inf
+            e = np.exp(s - np.where(some, m, 0.0)[:, None])
+            l = e.sum(axis=1)
+            p = e / np.where(some, l, 1.0)[:, None]
+            o[b, :, h], pv[b, :, h] = p @ vv, p @ np.abs(vv)
+            with np.errstate(divide="ignore"):
+                lse[b, h] = np.where(some, m + np.log(l), -np.inf)
+            size[b, h] = np.where(vis, np.abs(q[b, h]) @ np.abs(kk).T, 0.0).max(axis=1) / np.sqrt(dh)
     return o, pv, lse, size
 
 
@@ -63,13 +57,11 @@ def weigh(q, k, lse, lens, words, use, acc):
         if n0 < 0:
             continue
         seen = sees(None if words is None else words[b], N)
+        counts = np.array([use is None or bool((int(use[b][i // 32]) >> (i % 32)) & 1) for i in range(N)])
         for h in range(Hq):
-            for i in range(N):
-                if lse[b, h, i] == -np.inf or (use is not None and not (int(use[b][i // 32]) >> (i % 32)) & 1):
-                    continue
-                vis = np.concatenate([np.ones(n0, bool), seen[i]])
-                idx = np.flatnonzero(vis)
-                w[b, h // g, idx] += np.exp(k[b, h // g, idx] @ q[b, h, i] / np.sqrt(dh) - lse[b, h, i])
+            vis = np.concatenate([np.ones((N, n0), bool), seen], axis=1) & (counts & (lse[b, h] > -np.inf))[:, None]
+            x = q[b, h] @ k[b, h // g, :n0 + N].T / np.sqrt(dh) - np.where(lse[b, h] > -np.inf, lse[b, h], 0.0)[:, None]
+            w[b, h // g, :n0 + N] += np.exp(np.where(vis, x, -np.inf)).sum(axis=0)
         acc[b, :, :n0] += w[b, :, :n0]
         acc[b, :, n0:n0 + N] = w[b, :, n0:n0 + N]
     return acc, w

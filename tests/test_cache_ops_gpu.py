@@ -122,6 +122,11 @@ ATTEND = [
     (1, 8, 1, 256, 16, 5000, [4800], "tree"),                 # 128 rows, many tiles
     (40, 8, 8, 64, 1, 200, [150 + i % 40 for i in range(40)], "chain"),          # more units than SMs
     (33, 5, 5, 128, 4, 300, [(37 * i) % 297 for i in range(33)], "tree"),
+    # several tiles per CTA, segments that begin and end inside units, several row tiles
+    (3, 8, 1, 256, 63, 9000, [8900, 7001, 8555], "tree"),
+    (30, 4, 2, 256, 3, 3000, [2990 - 31 * i for i in range(30)], "tree"),
+    (12, 6, 2, 128, 130, 2300, [2100, -1, 2000, 300, 0, 2170, 1999, 5, 1500, 700, 2048, 129], "tree"),
+    (2, 34, 1, 64, 64, 6000, [5900, 3333], "chain"),          # 17 row tiles: two batches
 ]
 
 
@@ -222,7 +227,7 @@ def test_tree_attention_on_two_streams_with_their_own_workspaces():
     check(b, b.o, b.lse)
 
 
-WEIGH = [s for s in ATTEND if s[5] <= 5000]
+WEIGH = [s for s in ATTEND if s[5] <= 9000]
 
 
 @pytest.mark.parametrize("spec", WEIGH, ids=lambda s: "-".join(map(str, s[:6])) + "-" + s[7])
