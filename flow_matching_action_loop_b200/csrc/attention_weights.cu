@@ -46,9 +46,9 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ TileRange range;
-  __shared__ __align__(16) float lse_sh[AW_PASS];   // in log2 units, +inf: a row that gives nothing
+  __shared__ __align__(16) float lse_sh[AW_PASS];   // -lse in log2 units, -inf: a row that gives nothing
   __shared__ float half_sh[2][128];
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = a.Hq / a.Hkv, R = g * a.N;
   const int passes = (R + AW_PASS - 1) / AW_PASS;
   // the query rows of a pass take as many chunks as the largest pass has; the ring has the rest
@@ -57,6 +57,8 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
   uint8_t* ring = dsm + q_chunks * G::q_bytes;
 
   if (tid == 0) {
+    tma_prefetch_map(&a.tm_q);
+    tma_prefetch_map(&a.tm_k);
     for (int i = 0; i < AW_SLOTS; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tS = tmem_base;
+  const uint32_t tS = __shfl_sync(0xffffffffu, tmem_base, 0);
   volatile int* abort_v = &abort_flag;
   const TileRange rg = range;
   TileIter it;
@@ -128,59 +130,67 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
       if (q_use > 0) mbar_wait(&q_full, (q_use - 1) & 1, WAIT_LIMIT_NS);
     }
   } else if (warp == AW_SUM / 32 + 1) {
-    // ---------------- MMAs
-    if ((tid & 31) == 0) {
-      int slot = 0, use = 0, q_use = 0, item = 0;
-      while (ok && it.next(a, 1, 1, 0)) {
-        for (int p = 0; ok && p < passes; ++p) {
-          ok = mbar_wait(&q_full, q_use & 1, WAIT_LIMIT_NS);
-          ++q_use;
-          const int rows = pass_rows(p), nc = (rows + AW_CHUNK - 1) / AW_CHUNK;
-          for (int tile = it.tile0; ok && tile < it.tile1; ++tile) {
-            for (int c = 0; c < nc; ++c, ++item) {
-              const int buf = item % AW_BUFS, nth = item / AW_BUFS;
-              if (nth > 0 && !mbar_wait(&bar_e[buf], (nth - 1) & 1, WAIT_LIMIT_NS)) ok = false;
-              const int cols = (min(AW_CHUNK, rows - c * AW_CHUNK) + 31) & ~31;
-              const uint32_t idesc = idesc_f32acc(FMT_BF16, 128, cols);
-              const uint32_t qa = smem_u32(dsm + c * G::q_bytes);
-              int s = slot, u = use;
+    // ---------------- MMAs, the whole warp in step.  The waits go in a fixed order (bounded, in ok_wait).
+    const bool leader = elect_one();
+    auto ok_wait = [&](uint64_t* bar, int phase) {
+      if (__all_sync(0xffffffffu, mbar_test(bar, phase & 1))) return true;
+      return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, WAIT_LIMIT_NS) && !*abort_v) != 0;
+    };
+    auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };   // known to be uniform
+    const uint64_t dq = smem_desc_sw128(smem_u32(dsm), 16, 1024), dk = smem_desc_sw128(smem_u32(ring), 16, 1024);
+    int slot = 0, use = 0, q_use = 0, item = 0;
+    while (ok && same(it.next(a, 1, 1, 0))) {
+      const int tiles = same(it.tile1 - it.tile0);
+      for (int p = 0; ok && p < passes; ++p) {
+        ok = ok_wait(&q_full, q_use);
+        ++q_use;
+        const int rows = pass_rows(p), nc = (rows + AW_CHUNK - 1) / AW_CHUNK;
+        for (int tile = 0; ok && tile < tiles; ++tile) {
+          for (int c = 0; ok && c < nc; ++c, ++item) {
+            const int buf = item % AW_BUFS, nth = item / AW_BUFS;
+            if (nth > 0) ok = ok_wait(&bar_e[buf], nth - 1);
+            const int cols = (min(AW_CHUNK, rows - c * AW_CHUNK) + 31) & ~31;
+            const uint32_t idesc = idesc_f32acc(FMT_BF16, 128, cols), d = tS + buf * AW_CHUNK;
+            const uint64_t qd = dq + c * (G::q_bytes / 16);
+            int sl = slot, u = use;
 #pragma unroll
-              for (int i = 0; i < G::pieces; ++i) {
-                if (ok && c == 0) ok = mbar_wait(&full[s], u & 1, WAIT_LIMIT_NS) && !*abort_v;
-                if (!ok) break;
+            for (int i = 0; i < G::pieces; ++i) {
+              if (ok && c == 0) ok = ok_wait(&full[sl], u);
+              if (ok) {
                 tc_fence_after();
-                const uint32_t ka = smem_u32(ring + s * G::piece);
+                const uint64_t kd = dk + sl * (G::piece / 16);
 #pragma unroll
                 for (int k = 0; k < G::blocks * 4; ++k)
-                  mma_bf16(tS + buf * AW_CHUNK, smem_desc_sw128(ka + (k >> 2) * (TREE_KEYS * 128) + (k & 3) * 32, 16, 1024),
-                           smem_desc_sw128(qa + (i * G::blocks + (k >> 2)) * (AW_CHUNK * 128) + (k & 3) * 32, 16, 1024),
-                           idesc, i > 0 || k > 0);
-                if (c == nc - 1) mma_commit(&empty[s]);   // the tile's last rows
-                if (++s == NS) s = 0, ++u;
+                  mma_bf16_warp(leader, d, kd + ((k >> 2) * (TREE_KEYS * 128) + (k & 3) * 32) / 16,
+                                qd + ((i * G::blocks + (k >> 2)) * (AW_CHUNK * 128) + (k & 3) * 32) / 16, idesc,
+                                i > 0 || k > 0);
+                if (c == nc - 1) mma_commit_warp(leader, &empty[sl]);   // the tile's last rows
               }
-              if (!ok) break;
-              mma_commit(&bar_s[buf]);
+              if (++sl == NS) sl = 0, ++u;
             }
-            for (int i = 0; i < G::pieces; ++i)
-              if (++slot == NS) slot = 0, ++use;
+            if (ok) mma_commit_warp(leader, &bar_s[buf]);
           }
-          if (ok) mma_commit(&q_empty);
+#pragma unroll
+          for (int i = 0; i < G::pieces; ++i)
+            if (++slot == NS) slot = 0, ++use;
         }
+        if (ok) mma_commit_warp(leader, &q_empty);
       }
-      if (!ok) {
-        *abort_v = 1;
-        report_timeout(a.status, 0x721);
-      }
-      // every MMA issued has completed before tensor memory is freed
-      mma_commit(&fin_bar);
-      if (!mbar_wait(&fin_bar, 0, WAIT_LIMIT_NS)) report_timeout(a.status, 0x722);
     }
+    if (!ok) {
+      *abort_v = 1;
+      if (leader) report_timeout(a.status, 0x721);
+    }
+    // every MMA issued has completed before tensor memory is freed
+    mma_commit_warp(leader, &fin_bar);
+    if (!mbar_wait(&fin_bar, 0, WAIT_LIMIT_NS) && leader) report_timeout(a.status, 0x722);
   } else {
     // ---------------- sums.  A warp whose wait gave up goes on without waiting (the named barriers need
     // every warp) and stores nothing.
     const int key = tid & 127, hh = tid >> 7, pw = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(pw * 32) << 16;
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in log2 units
+    const uint64_t sl22 = pack_f32x2(sl2, sl2);
     int item = 0;
     while (it.next(a, 1, 1, 0)) {
       const int len = it.len, keys = len + a.N;
@@ -190,12 +200,12 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
         const int rows = pass_rows(p), nc = (rows + AW_CHUNK - 1) / AW_CHUNK, r0 = p * AW_PASS;
         asm volatile("bar.sync 5, 256;" ::: "memory");   // the last pass has read its lse
         {
-          float x = INFINITY;
+          float x = -INFINITY;
           if (tid < rows) {
             const int n = (r0 + tid) % a.N;
             const bool counts = !a.use || ((a.use[static_cast<size_t>(it.b) * a.W + (n >> 5)] >> (n & 31)) & 1u);
             const float v = lse[r0 + tid];
-            if (counts && v != -INFINITY) x = v * 1.4426950408889634f;
+            if (counts && v != -INFINITY) x = -v * 1.4426950408889634f;
           }
           lse_sh[tid] = x;
         }
@@ -205,10 +215,12 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
           const bool boundary = (tile + 1) * TREE_KEYS > len;
           // committed slots add to their sum; drafted ones begin with the first rows
           const float before = hh == 0 && slot < keys && (slot < len || p > 0) ? acc[slot] : 0.f;
-          float w[4] = {0.f, 0.f, 0.f, 0.f};
+          float w = 0.f;
+          uint64_t w2[2] = {0, 0};
           for (int c = 0; c < nc; ++c, ++item) {
             const int buf = item % AW_BUFS;
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bar_s[buf], (item / AW_BUFS) & 1, WAIT_LIMIT_NS) && !*abort_v);
+            if (!__all_sync(0xffffffffu, mbar_test(&bar_s[buf], (item / AW_BUFS) & 1)) && ok)
+              ok = __all_sync(0xffffffffu, mbar_wait(&bar_s[buf], (item / AW_BUFS) & 1, WAIT_LIMIT_NS) && !*abort_v);
             tc_fence_after();
             const int half = ((min(AW_CHUNK, rows - c * AW_CHUNK) + 31) & ~31) / 2;   // columns of this thread
             const uint32_t ts = tS + buf * AW_CHUNK + lanes + hh * half;
@@ -217,10 +229,12 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
 #pragma unroll
               for (int e = 0; e < 16; e += 4) {
                 const float4 l4 = *reinterpret_cast<const float4*>(ls + col + e);
-                w[0] += ex2_approx(fmaf(__uint_as_float(s[e]), sl2, -l4.x));
-                w[1] += ex2_approx(fmaf(__uint_as_float(s[e + 1]), sl2, -l4.y));
-                w[2] += ex2_approx(fmaf(__uint_as_float(s[e + 2]), sl2, -l4.z));
-                w[3] += ex2_approx(fmaf(__uint_as_float(s[e + 3]), sl2, -l4.w));
+                const float2 x = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl22,
+                                                        pack_f32x2(l4.x, l4.y)));
+                const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), sl22,
+                                                        pack_f32x2(l4.z, l4.w)));
+                w2[0] = add_f32x2(w2[0], pack_f32x2(ex2_approx(x.x), ex2_approx(x.y)));
+                w2[1] = add_f32x2(w2[1], pack_f32x2(ex2_approx(y.x), ex2_approx(y.y)));
               }
             };
             if (!boundary) {
@@ -256,7 +270,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
                   if (!sees && j < a.N)
                     sees = a.mask ? (a.mask[(static_cast<size_t>(it.b) * a.N + n) * a.W + (j >> 5)] >> (j & 31)) & 1u : j <= n;
                   const float l = ls[col + e];
-                  if (sees && l != INFINITY) w[e & 3] += ex2_approx(fmaf(__uint_as_float(s[e]), sl2, -l));
+                  if (sees && l != -INFINITY) w += ex2_approx(fmaf(__uint_as_float(s[e]), sl2, l));
                   if (++n == a.N) n = 0;
                 }
               }
@@ -265,7 +279,8 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
             __syncwarp();
             if ((tid & 31) == 0) mbar_arrive(&bar_e[buf]);
           }
-          const float mine = (w[0] + w[1]) + (w[2] + w[3]);
+          const float2 wp = unpack_f32x2(add_f32x2(w2[0], w2[1]));
+          const float mine = w + (wp.x + wp.y);
           if (hh == 1) half_sh[tile & 1][key] = mine;
           asm volatile("bar.sync %0, 64;" ::"r"(1 + pw) : "memory");
           if (hh == 0 && slot < keys && ok) acc[slot] = before + (mine + half_sh[tile & 1][key]);

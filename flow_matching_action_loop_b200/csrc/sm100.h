@@ -105,6 +105,10 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const void* tmap, in
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
+// Brings a tensor map to the copy engine ahead of its first copy.
+__device__ __forceinline__ void tma_prefetch_map(const void* tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
+}
 // L2 cache policy for data read once per pass (streamed weights): evicted first, so that the
 // activations, partials and the KV cache stay resident.
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {

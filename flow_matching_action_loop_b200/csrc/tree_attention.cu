@@ -121,6 +121,9 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
   // The copy warp finds the CTA's tiles and starts the first copies while warp 0 allocates tensor memory.
   if (warp == TA_SOFTMAX / 32) {
     if ((tid & 31) == 0) {
+      tma_prefetch_map(&a.tm_q);
+      tma_prefetch_map(&a.tm_k);
+      tma_prefetch_map(&a.tm_v);
       for (int i = 0; i < G::NS; ++i) {
         mbar_init(&full[i], 1);
         mbar_init(&empty[i], 1);
@@ -586,7 +589,7 @@ __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant
     for (int e = 0; e < 16; ++e) o[e] = o[e] * w0 + v[e] * w1;
   };
   if (row < Rv) {
-    constexpr int UN = 2;   // segments in flight
+    constexpr int UN = 4;   // segments in flight
     for (int cb = c0 + sub; cb <= c1; cb += UN * split) {
       float4 v[UN][4], st[UN];
 #pragma unroll
@@ -653,7 +656,7 @@ cudaError_t launch_tree(TreeArgs& a, cudaStream_t s) {
   // segments per unit if every sample is as long as can be
   const int64_t units = static_cast<int64_t>(planes) * ((RT + a.rtg - 1) / a.rtg);
   const int per = static_cast<int>(a.groups / std::min<int64_t>(units, a.groups)) + 1;
-  const int split = per > 32 ? 8 : per > 16 ? 4 : per > 8 ? 2 : 1;
+  const int split = per > 16 ? 8 : per > 8 ? 4 : per > 4 ? 2 : 1;
   const int rows = TM_THREADS / (DH / 16) / split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((std::min(R, 128) + rows - 1) / rows, a.Hkv * RT, a.B);
