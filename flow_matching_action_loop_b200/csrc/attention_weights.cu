@@ -3,14 +3,16 @@
 // With the log-sum-exp of every row known, slot s's weight is a sum over rows of independent terms,
 // exp(q k_s / sqrt(dh) - lse).  The scores are computed transposed, K Q^T: a lane of tensor memory is a
 // slot and a column a row, so that each thread sums the terms of one slot in registers and nothing is
-// exchanged but the two halves of the columns; there are no atomics.
+// exchanged; there are no atomics.
 //
 // The 128-slot tiles of all (sample, KV head) pairs form one line, cut into equal ranges over the CTAs (one
 // per SM).  A CTA keeps up to 256 of the pair's rows in shared memory and streams its K tiles past them
 // (from the second 256 rows on out of the L2); a slot's sum is added to acc by the same thread each time.
 //   copy warp      query rows, K tiles by tensor map (128-byte swizzle) into a ring
-//   MMA warp       K(t) Q^T, 128 rows at a time, into one of four score buffers in tensor memory
-//   sum warps (8)  two threads per slot, half of the columns each: 2^(s - lse) in fp32
+//   MMA warp       K(t) Q^T, 128 rows at a time, into one of a sum group's two score buffers in tensor memory
+//   sum warps      two groups of four take the tiles in turn, a thread a slot: 2^(s - lse) in fp32.  (With
+//                  both groups on one tile, half of the columns each, a tile's exponentials had nothing to
+//                  overlap with: 1870 cycles for 128 x 128 scores against 1024 of the exponentials.)
 #include <algorithm>
 
 #include "fr.h"
@@ -26,7 +28,6 @@ constexpr int AW_SUM = 256;
 constexpr int AW_THREADS = AW_SUM + 64;
 constexpr int AW_CHUNK = 128;               // rows per score buffer
 constexpr int AW_PASS = 2 * AW_CHUNK;       // rows held in shared memory
-constexpr int AW_BUFS = 4;                  // score buffers
 constexpr int AW_SLOTS = 10;                // ring slots at most
 constexpr int AW_SMEM = 224 * 1024;
 
@@ -42,12 +43,11 @@ template <int DH>
 __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_constant__ TreeArgs a) {
   using G = WeightGeom<DH>;
   extern __shared__ __align__(1024) uint8_t dsm[];
-  __shared__ uint64_t full[AW_SLOTS], empty[AW_SLOTS], q_full, q_empty, bar_s[AW_BUFS], bar_e[AW_BUFS], fin_bar;
+  __shared__ uint64_t full[AW_SLOTS], empty[AW_SLOTS], q_full, q_empty, bar_s[4], bar_e[4], fin_bar;   // [2 x group + buffer]
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ TileRange range;
   __shared__ __align__(16) float lse_sh[AW_PASS];   // -lse in log2 units, -inf: a row that gives nothing
-  __shared__ float half_sh[2][128];
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = a.Hq / a.Hkv, R = g * a.N;
   const int passes = (R + AW_PASS - 1) / AW_PASS;
@@ -63,9 +63,9 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < AW_BUFS; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&bar_s[i], 1);
-      mbar_init(&bar_e[i], AW_SUM / 32);
+      mbar_init(&bar_e[i], 4);
     }
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
@@ -138,17 +138,18 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
     };
     auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };   // known to be uniform
     const uint64_t dq = smem_desc_sw128(smem_u32(dsm), 16, 1024), dk = smem_desc_sw128(smem_u32(ring), 16, 1024);
-    int slot = 0, use = 0, q_use = 0, item = 0;
+    int slot = 0, use = 0, q_use = 0, grp = 0, items[2] = {0, 0};   // group of the next tile, items of each group
     while (ok && same(it.next(a, 1, 1, 0))) {
       const int tiles = same(it.tile1 - it.tile0);
       for (int p = 0; ok && p < passes; ++p) {
         ok = ok_wait(&q_full, q_use);
         ++q_use;
         const int rows = pass_rows(p), nc = (rows + AW_CHUNK - 1) / AW_CHUNK;
-        for (int tile = 0; ok && tile < tiles; ++tile) {
+        for (int tile = 0; ok && tile < tiles; ++tile, grp ^= 1) {
+          int item = grp ? items[1] : items[0];
           for (int c = 0; ok && c < nc; ++c, ++item) {
-            const int buf = item % AW_BUFS, nth = item / AW_BUFS;
-            if (nth > 0) ok = ok_wait(&bar_e[buf], nth - 1);
+            const int buf = 2 * grp + (item & 1), nth = item >> 1;
+            if (nth > 0) ok = ok_wait(&bar_e[buf], nth - 1);   // its scores before these have been read
             const int cols = (min(AW_CHUNK, rows - c * AW_CHUNK) + 31) & ~31;
             const uint32_t idesc = idesc_f32acc(FMT_BF16, 128, cols), d = tS + buf * AW_CHUNK;
             const uint64_t qd = dq + c * (G::q_bytes / 16);
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
             }
             if (ok) mma_commit_warp(leader, &bar_s[buf]);
           }
+          (grp ? items[1] : items[0]) = item;
 #pragma unroll
           for (int i = 0; i < G::pieces; ++i)
             if (++slot == NS) slot = 0, ++use;
@@ -185,13 +187,13 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
     mma_commit_warp(leader, &fin_bar);
     if (!mbar_wait(&fin_bar, 0, WAIT_LIMIT_NS) && leader) report_timeout(a.status, 0x722);
   } else {
-    // ---------------- sums.  A warp whose wait gave up goes on without waiting (the named barriers need
+    // ---------------- sums.  A warp whose wait gave up goes on without waiting (the named barrier needs
     // every warp) and stores nothing.
-    const int key = tid & 127, hh = tid >> 7, pw = warp & 3;
+    const int key = tid & 127, grp = tid >> 7, pw = warp & 3, lane = tid & 31;   // slot of the tile, group
     const uint32_t lanes = static_cast<uint32_t>(pw * 32) << 16;
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in log2 units
     const uint64_t sl22 = pack_f32x2(sl2, sl2);
-    int item = 0;
+    int item = 0, turn = 0;                            // of this group; group of the next tile
     while (it.next(a, 1, 1, 0)) {
       const int len = it.len, keys = len + a.N;
       float* acc = a.acc + (static_cast<size_t>(it.b) * a.Hkv + it.hk) * a.S_max;
@@ -210,24 +212,58 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
           lse_sh[tid] = x;
         }
         asm volatile("bar.sync 5, 256;" ::: "memory");
-        for (int tile = it.tile0; tile < it.tile1; ++tile) {
+        // a committed slot adds to its sum, a drafted one begins with the first rows; fetched a tile ahead
+        auto sum_before = [&](int tile) {
+          const int slot = tile * TREE_KEYS + key;
+          return tile < it.tile1 && slot < keys && (slot < len || p > 0) ? acc[slot] : 0.f;
+        };
+        const int first = it.tile0 + (turn ^ grp);   // this group's tiles: every other one
+        turn ^= (it.tile1 - it.tile0) & 1;
+        float before = sum_before(first);
+        for (int tile = first; tile < it.tile1; tile += 2) {
           const int slot = tile * TREE_KEYS + key;
           const bool boundary = (tile + 1) * TREE_KEYS > len;
-          // committed slots add to their sum; drafted ones begin with the first rows
-          const float before = hh == 0 && slot < keys && (slot < len || p > 0) ? acc[slot] : 0.f;
-          float w = 0.f;
+          const float next = sum_before(tile + 2);
           uint64_t w2[2] = {0, 0};
           for (int c = 0; c < nc; ++c, ++item) {
-            const int buf = item % AW_BUFS;
-            if (!__all_sync(0xffffffffu, mbar_test(&bar_s[buf], (item / AW_BUFS) & 1)) && ok)
-              ok = __all_sync(0xffffffffu, mbar_wait(&bar_s[buf], (item / AW_BUFS) & 1, WAIT_LIMIT_NS) && !*abort_v);
-            tc_fence_after();
-            const int half = ((min(AW_CHUNK, rows - c * AW_CHUNK) + 31) & ~31) / 2;   // columns of this thread
-            const uint32_t ts = tS + buf * AW_CHUNK + lanes + hh * half;
-            const float* ls = lse_sh + c * AW_CHUNK + hh * half;
-            auto sum16 = [&](const uint32_t* s, int col) {
+            const int buf = 2 * grp + (item & 1);
+            const int cols = (min(AW_CHUNK, rows - c * AW_CHUNK) + 31) & ~31;
+            const float* ls = lse_sh + c * AW_CHUNK;
+            // columns (rows) that see this thread's slot: a lane finds the 32 slots of its warp that its
+            // column sees, a transposition of the 32 x 32 bits gives each slot its columns
+            uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+            if (boundary) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) {
+              for (int i = 0; i < 4; ++i) {
+                const int col = 32 * i + lane;
+                uint32_t x = 0;
+                if (col < cols && ls[col] != -INFINITY) {
+                  const int n = (r0 + c * AW_CHUNK + col) % a.N;
+                  const uint32_t* words = a.mask ? a.mask + (static_cast<size_t>(it.b) * a.N + n) * a.W : nullptr;
+                  x = seen_slots(words, n, a.N, tile * TREE_KEYS + 32 * pw - len);
+                }
+#pragma unroll
+                for (int st = 16; st; st >>= 1) {
+                  const uint32_t m = st == 16 ? 0x0000ffffu : st == 8 ? 0x00ff00ffu : st == 4 ? 0x0f0f0f0fu
+                                   : st == 2 ? 0x33333333u : 0x55555555u;
+                  const uint32_t y = __shfl_xor_sync(0xffffffffu, x, st);
+                  x = lane & st ? (x & ~m) | ((y >> st) & m) : (x & m) | ((y & m) << st);
+                }
+                vis[i] = x;
+              }
+            }
+            if (!__all_sync(0xffffffffu, mbar_test(&bar_s[buf], (item >> 1) & 1)) && ok)
+              ok = __all_sync(0xffffffffu, mbar_wait(&bar_s[buf], (item >> 1) & 1, WAIT_LIMIT_NS) && !*abort_v);
+            tc_fence_after();
+            const uint32_t ts = tS + buf * AW_CHUNK + lanes;
+            auto sum32 = [&](uint32_t* s, int col, uint32_t v) {
+              if (boundary) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((v >> e) & 1u)) s[e] = 0xff800000u;   // -inf
+              }
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
                 const float4 l4 = *reinterpret_cast<const float4*>(ls + col + e);
                 const float2 x = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl22,
                                                         pack_f32x2(l4.x, l4.y)));
@@ -237,53 +273,25 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
                 w2[1] = add_f32x2(w2[1], pack_f32x2(ex2_approx(y.x), ex2_approx(y.y)));
               }
             };
-            if (!boundary) {
-              if (half == 64) {
-                uint32_t s[64];
-                tmem_ld32_nowait(ts, s);
-                tmem_ld32_nowait(ts + 32, s + 32);
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if ((tid & 31) == 0) mbar_arrive(&bar_e[buf]);
+            uint32_t s0[32], s1[32];
+            tmem_ld32_nowait(ts, s0);
+            tmem_wait_ld();
 #pragma unroll
-                for (int col = 0; col < 64; col += 16) sum16(s + col, col);
-                continue;
-              }
-              for (int col = 0; col < half; col += 16) {
-                uint32_t s[16];
-                tmem_ld16_nowait(ts + col, s);
+            for (int i = 0; i < 4; ++i) {   // 32 columns at a time, the next ones on their way
+              if (32 * i < cols) {
+                uint32_t* now = i & 1 ? s1 : s0;
+                if (32 * (i + 1) < cols) tmem_ld32_nowait(ts + 32 * (i + 1), i & 1 ? s0 : s1);
+                sum32(now, 32 * i, vis[i]);
                 tmem_wait_ld();
-                sum16(s, col);
-              }
-            } else {
-              // a drafted slot counts for the rows whose token sees it
-              const int j = slot - len;
-              int n = (r0 + c * AW_CHUNK + hh * half) % a.N;
-              for (int col = 0; col < half; col += 16) {
-                uint32_t s[16];
-                tmem_ld16_nowait(ts + col, s);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  bool sees = j < 0;
-                  if (!sees && j < a.N)
-                    sees = a.mask ? (a.mask[(static_cast<size_t>(it.b) * a.N + n) * a.W + (j >> 5)] >> (j & 31)) & 1u : j <= n;
-                  const float l = ls[col + e];
-                  if (sees && l != -INFINITY) w += ex2_approx(fmaf(__uint_as_float(s[e]), sl2, l));
-                  if (++n == a.N) n = 0;
-                }
               }
             }
             tc_fence_before();
             __syncwarp();
-            if ((tid & 31) == 0) mbar_arrive(&bar_e[buf]);
+            if (lane == 0) mbar_arrive(&bar_e[buf]);
           }
           const float2 wp = unpack_f32x2(add_f32x2(w2[0], w2[1]));
-          const float mine = w + (wp.x + wp.y);
-          if (hh == 1) half_sh[tile & 1][key] = mine;
-          asm volatile("bar.sync %0, 64;" ::"r"(1 + pw) : "memory");
-          if (hh == 0 && slot < keys && ok) acc[slot] = before + (mine + half_sh[tile & 1][key]);
+          if (slot < keys && ok) acc[slot] = before + (wp.x + wp.y);
+          before = next;
         }
       }
     }
