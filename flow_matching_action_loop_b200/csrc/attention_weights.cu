@@ -213,10 +213,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
         }
         asm volatile("bar.sync 5, 256;" ::: "memory");
         // a committed slot adds to its sum, a drafted one begins with the first rows; fetched a tile ahead
-        auto sum_before = [&](int tile) {
-          const int slot = tile * TREE_KEYS + key;
-          return tile < it.tile1 && slot < keys && (slot < len || p > 0) ? acc[slot] : 0.f;
-        };
+        auto sum_before = [&](int tile) { return acc[min(tile * TREE_KEYS + key, keys - 1)]; };
         const int first = it.tile0 + (turn ^ grp);   // this group's tiles: every other one
         turn ^= (it.tile1 - it.tile0) & 1;
         float before = sum_before(first);
@@ -235,13 +232,13 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
             if (boundary) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int col = 32 * i + lane;
-                uint32_t x = 0;
-                if (col < cols && ls[col] != -INFINITY) {
-                  const int n = (r0 + c * AW_CHUNK + col) % a.N;
-                  const uint32_t* words = a.mask ? a.mask + (static_cast<size_t>(it.b) * a.N + n) * a.W : nullptr;
-                  x = seen_slots(words, n, a.N, tile * TREE_KEYS + 32 * pw - len);
-                }
+                const int n = (r0 + c * AW_CHUNK + 32 * i + lane) % a.N;
+                const uint32_t* words = a.mask ? a.mask + (static_cast<size_t>(it.b) * a.N + n) * a.W : nullptr;
+                vis[i] = seen_slots(words, n, a.N, a.W, tile * TREE_KEYS + 32 * pw - len);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t x = ls[32 * i + lane] != -INFINITY ? vis[i] : 0u;
 #pragma unroll
                 for (int st = 16; st; st >>= 1) {
                   const uint32_t m = st == 16 ? 0x0000ffffu : st == 8 ? 0x00ff00ffu : st == 4 ? 0x0f0f0f0fu
@@ -290,7 +287,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
             if (lane == 0) mbar_arrive(&bar_e[buf]);
           }
           const float2 wp = unpack_f32x2(add_f32x2(w2[0], w2[1]));
-          if (slot < keys && ok) acc[slot] = before + (wp.x + wp.y);
+          if (slot < keys && ok) acc[slot] = (slot < len || p > 0 ? before : 0.f) + (wp.x + wp.y);
           before = next;
         }
       }

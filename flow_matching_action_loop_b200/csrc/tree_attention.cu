@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (boundary) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vis[i] = seen_slots(words, tok, a.N, key0 + 32 * i - len);
+          for (int i = 0; i < 4; ++i) vis[i] = seen_slots(words, tok, a.N, a.W, key0 + 32 * i - len);
         }
         wait(&bar_s[t & 1], (t >> 1) & 1);
         const uint32_t ts = tS + (t % G::LA) * TREE_KEYS + lanes, tp = tP + (t & 1) * 64 + lanes;

@@ -153,21 +153,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Word i of the drafted tokens that token n sees, from its mask row (nullptr: tokens 0..n).
-__device__ __forceinline__ uint32_t seen_word(const uint32_t* row, int n, int N, int i) {
-  if (32 * i >= N || i < 0) return 0u;
-  const uint32_t last = 32 * i + 32 > N ? (1u << (N - 32 * i)) - 1u : 0xffffffffu;
-  if (row) return row[i] & last;
-  return n >= 32 * i + 31 ? last : n < 32 * i ? 0u : ((2u << (n - 32 * i)) - 1u) & last;
+// Word i of what token n sees of the slots from the first drafted one on, from its mask row of W words
+// (nullptr: tokens 0..n); before it committed slots, after the N drafted ones nothing.  The load has no
+// branch before it, so that several calls' loads are on their way together.
+__device__ __forceinline__ uint32_t seen_word(const uint32_t* row, int n, int N, int W, int i) {
+  uint32_t w = row ? row[min(max(i, 0), W - 1)] : 0xffffffffu;
+  if (!row) w = n >= 32 * i + 31 ? 0xffffffffu : n < 32 * i ? 0u : (2u << (n & 31)) - 1u;
+  const uint32_t in = 32 * i + 32 <= N ? 0xffffffffu : 32 * i >= N ? 0u : (1u << (N & 31)) - 1u;
+  return i < 0 ? 0xffffffffu : w & in;
 }
 
 // Bits t = 0..31: token n sees the slot of drafted index j0 + t (negative: committed, seen).
-__device__ __forceinline__ uint32_t seen_slots(const uint32_t* row, int n, int N, int j0) {
-  if (j0 <= -32) return 0xffffffffu;
-  if (j0 >= N) return 0u;
-  if (j0 < 0) return ((1u << -j0) - 1u) | (seen_word(row, n, N, 0) << -j0);
-  const uint32_t lo = seen_word(row, n, N, j0 >> 5), hi = seen_word(row, n, N, (j0 >> 5) + 1);
-  return __funnelshift_r(lo, hi, j0 & 31);
+__device__ __forceinline__ uint32_t seen_slots(const uint32_t* row, int n, int N, int W, int j0) {
+  return __funnelshift_r(seen_word(row, n, N, W, j0 >> 5), seen_word(row, n, N, W, (j0 >> 5) + 1), j0 & 31);
 }
 
 // Tensor map of [planes][rows][dh] bf16 (rows contiguous, planes plane_rows apart) for one copy of
