@@ -237,17 +237,21 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
                 vis[i] = seen_slots(words, n, a.N, a.W, tile * TREE_KEYS + 32 * pw - len);
               }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t x = ls[32 * i + lane] != -INFINITY ? vis[i] : 0u;
+              for (int i = 0; i < 4; ++i)
+                if (ls[32 * i + lane] == -INFINITY) vis[i] = 0;
+              auto stage = [&](int st, uint32_t m) {   // the four words side by side: a shuffle waits long
+                uint32_t y[4];
 #pragma unroll
-                for (int st = 16; st; st >>= 1) {
-                  const uint32_t m = st == 16 ? 0x0000ffffu : st == 8 ? 0x00ff00ffu : st == 4 ? 0x0f0f0f0fu
-                                   : st == 2 ? 0x33333333u : 0x55555555u;
-                  const uint32_t y = __shfl_xor_sync(0xffffffffu, x, st);
-                  x = lane & st ? (x & ~m) | ((y >> st) & m) : (x & m) | ((y & m) << st);
-                }
-                vis[i] = x;
-              }
+                for (int i = 0; i < 4; ++i) y[i] = __shfl_xor_sync(0xffffffffu, vis[i], st);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  vis[i] = lane & st ? (vis[i] & ~m) | ((y[i] >> st) & m) : (vis[i] & m) | ((y[i] & m) << st);
+              };
+              stage(16, 0x0000ffffu);
+              stage(8, 0x00ff00ffu);
+              stage(4, 0x0f0f0f0fu);
+              stage(2, 0x33333333u);
+              stage(1, 0x55555555u);
             }
             if (!__all_sync(0xffffffffu, mbar_test(&bar_s[buf], (item >> 1) & 1)) && ok)
               ok = __all_sync(0xffffffffu, mbar_wait(&bar_s[buf], (item >> 1) & 1, WAIT_LIMIT_NS) && !*abort_v);
