@@ -38,7 +38,11 @@ namespace {
 using namespace fr::sm100;
 
 constexpr int TA_SOFTMAX = 256;                // softmax threads
-constexpr int TA_THREADS = TA_SOFTMAX + 64;    // + the copy warp and the MMA warp
+constexpr int TA_THREADS = TA_SOFTMAX + 128;   // + a warpgroup of the copy warp and the MMA warp
+// Registers: 384 threads are launched with 168 each; a softmax thread holds a row's 128 scores, so that the
+// score buffer is free as soon as they are loaded.
+constexpr int TA_REGS = 168, TA_REGS_SOFTMAX = 208, TA_REGS_OTHER = 88;
+static_assert(2 * TA_REGS_SOFTMAX + TA_REGS_OTHER == 3 * TA_REGS, "registers are only moved");
 constexpr int TA_CTAS = 148;                   // at most: the scratch holds two segments' rows for each
 constexpr float TA_RESCALE = 8.f;
 
@@ -167,6 +171,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
   TileIter it = first_seg;
   bool more = any_seg != 0;
 
+  if (warp >= TA_SOFTMAX / 32) {
+    regs_shrink<TA_REGS_OTHER>();
   if (warp == TA_SOFTMAX / 32) {
     // ---------------- copies: pieces in the order the MMA warp takes them, K(0) .. K(LA-1), then K(t+LA), V(t).
     // The places of K tiles past the last are left out, so that V(t) is always at pieces * (2 t + LA + 1).
@@ -213,20 +219,22 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
   } else if (warp == TA_SOFTMAX / 32 + 1) {
     // ---------------- MMAs, the whole warp in step
     if (more) {
-      // S runs up to LA tiles ahead of P V.  Whichever has what it waits for is issued next, S first (a
-      // softmax group may wait for it); in a fixed order S(t+LA) waited for the softmax of tile t-1.
-      // A barrier is tested only where its phase before is known to have completed.
+      // S runs ahead of P V.  Whichever has what it waits for is issued next, S first (a softmax group may
+      // wait for it); in a fixed order S(t+LA) waited for the softmax of tile t-1.  A barrier tells a phase
+      // from the one two before it only if the phase between is known to have completed.  The place of
+      // K(ts) in the ring held, NS places before, V(tv - 2) or an earlier tile as long as ts <= tv + LA + 1,
+      // and P V has been issued up to tv - 1: so S runs at most that far ahead.
       const bool leader = elect_one();
       auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };   // known to be uniform
       TileIter vi = it;
       int ts = 0, tv = 0, seg_s = 0;                        // next S and P V, query tile
       int st = same(it.tile1 - it.tile0), vt = st;          // tiles left of their segments
       bool more_s = true, s_begins = true, v_begins = true; // a segment begins with the tile
-      auto test = [](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)); };
+      auto test = [](uint64_t* bar, int phase) { return static_cast<unsigned>(mbar_test(bar, phase & 1)); };
       auto landed = [&](int p) {   // a tile's pieces, from ring position p on
-        bool r = true;
+        unsigned r = 1u;
 #pragma unroll
-        for (int i = 0; i < G::pieces; ++i) r = r && test(&full[(p + i) % G::NS], (p + i) / G::NS);
+        for (int i = 0; i < G::pieces; ++i) r &= test(&full[(p + i) % G::NS], (p + i) / G::NS);
         return r;
       };
       const uint64_t dq = smem_desc_sw128(smem_u32(dsm), 16, 1024), dk = smem_desc_sw128(smem_u32(ring), 16, 1024),
@@ -234,8 +242,16 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
       uint64_t idle = 0;
       for (;;) {
         const int pk = G::pieces * (ts < G::LA ? ts : 2 * ts - G::LA), pv = G::pieces * (2 * tv + G::LA + 1);
-        if (more_s && (!s_begins || test(&q_full[seg_s % G::QB], seg_s / G::QB)) &&
-            (ts < G::LA || test(&bar_l[(ts - G::LA) & 1], (ts - G::LA) >> 1)) && landed(pk)) {
+        // every test is on its way before the first answer is used: one after the other they took 700 cycles
+        unsigned s_ok = more_s && ts <= tv + G::LA + 1, v_ok = tv < ts;
+        if (s_ok) {
+          s_ok = landed(pk);
+          if (ts >= G::LA) s_ok &= test(&bar_l[(ts - G::LA) & 1], (ts - G::LA) >> 1);
+          if (s_begins) s_ok &= test(&q_full[seg_s % G::QB], seg_s / G::QB);
+        }
+        if (v_ok) v_ok = landed(pv) & test(&bar_p[tv & 1], tv >> 1);
+        const bool s_go = __all_sync(0xffffffffu, s_ok), v_go = __all_sync(0xffffffffu, v_ok);
+        if (s_go) {
           tc_fence_after();
           const uint64_t qd = dq + (seg_s % G::QB) * (G::q_bytes / 16);
           const uint32_t d = tS + (ts % G::LA) * TREE_KEYS;
@@ -258,7 +274,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
             s_begins = true;
             ++seg_s;
           }
-        } else if (tv < ts && test(&bar_p[tv & 1], tv >> 1) && landed(pv)) {
+        } else if (v_go) {
           tc_fence_after();
           // steps of 16 slots: those that hold slots in use
           const int steps = same(min(TREE_KEYS, vi.len + a.N - (vi.tile1 - vt) * TREE_KEYS + 15) / 16);
@@ -301,7 +317,9 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
       mma_commit_warp(leader, &fin_bar);
       if (!mbar_wait(&fin_bar, 0, WAIT_LIMIT_NS) && leader) report_timeout(a.status, 0x712);
     }
+  }
   } else {
+    regs_grow<TA_REGS_SOFTMAX>();
     // ---------------- softmax.  A warp whose wait gave up goes on without waiting (the named barriers
     // need every warp) and stores nothing.
     const int row = tid & 127, hh = tid >> 7, pw = warp & 3;   // row of the tile, group, lane quadrant
@@ -336,34 +354,23 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         float corr = 1.f, off = 0.f;
         const uint64_t sl22 = pack_f32x2(sl2, sl2);
         uint64_t ps[2] = {0, 0};
-        uint32_t s[64];
-        // half of the row's scores, 64 * half on, hidden ones -inf
-        auto load = [&](int half) {
-          tmem_ld32_nowait(ts + 64 * half, s);
-          tmem_ld32_nowait(ts + 64 * half + 32, s + 32);
+        uint32_t s[128];
+        if (work) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32_nowait(ts + 32 * i, s + 32 * i);
           tmem_wait_ld();
-          if (boundary) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (!(((half ? vis[2 + (e >> 5)] : vis[e >> 5]) >> (e & 31)) & 1u)) s[e] = 0xff800000u;
-          }
-        };
-        auto maximum = [&]() {
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            float& m = m4[(e >> 1) & 3];
-            m = max3(m, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-          }
-          return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        };
-        auto weights = [&](int half) {   // P of half a row
+          tc_fence_before();
+        }
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(&bar_l[t & 1]);
+        auto weights = [&](auto which) {   // P of half a row
+          constexpr int half = decltype(which)::value;
           const uint64_t off2 = pack_f32x2(-off, -off);
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
-            const float2 x = unpack_f32x2(
-                fma_f32x2(pack_f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl22, off2));
+            const float2 x = unpack_f32x2(fma_f32x2(
+                pack_f32x2(__uint_as_float(s[64 * half + e]), __uint_as_float(s[64 * half + e + 1])), sl22, off2));
             const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
             ps[(e >> 1) & 1] = add_f32x2(ps[(e >> 1) & 1], pack_f32x2(p0, p1));
             pk[e >> 1] = pack_bf16x2(p0, p1);
@@ -371,10 +378,18 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
           tmem_st32(tp + 32 * half, pk);
         };
         if (work) {
-          load(0);
-          float mx = maximum();
-          load(1);
-          mx = fmaxf(mx, maximum()) * sl2;
+          if (boundary) {
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (!((vis[e >> 5] >> (e & 31)) & 1u)) s[e] = 0xff800000u;   // -inf
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 128; e += 2) {
+            float& m = m4[(e >> 1) & 3];
+            m = max3(m, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          }
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
           // the reference after the tile before this one: the other group's
           float before = -INFINITY;
           if (tile > it.tile0) {
@@ -395,14 +410,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         }
         wait(&bar_o[t & 1], ((t >> 1) - 1) & 1);   // P(t - 2) has been read
         if (work) {
-          weights(1);
-          load(0);
-          tc_fence_before();
-        }
-        __syncwarp();
-        if ((tid & 31) == 0) mbar_arrive(&bar_l[t & 1]);
-        if (work) {
-          weights(0);
+          weights(std::integral_constant<int, 0>{});
+          weights(std::integral_constant<int, 1>{});
           const float2 pt = unpack_f32x2(add_f32x2(ps[0], ps[1]));
           l += pt.x + pt.y;
           if (tile > it.tile0 && __any_sync(0xffffffffu, corr != 1.f)) {

@@ -127,6 +127,8 @@ ATTEND = [
     (30, 4, 2, 256, 3, 3000, [2990 - 31 * i for i in range(30)], "tree"),
     (12, 6, 2, 128, 130, 2300, [2100, -1, 2000, 300, 0, 2170, 1999, 5, 1500, 700, 2048, 129], "tree"),
     (2, 34, 1, 64, 64, 6000, [5900, 3333], "chain"),          # 17 row tiles: two batches
+    # single tokens over a cache that streams from memory: tiles land late and out of order
+    (24, 32, 8, 128, 1, 4200, [4190 - 97 * i for i in range(24)], "chain"),
 ]
 
 
@@ -227,7 +229,7 @@ def test_tree_attention_on_two_streams_with_their_own_workspaces():
     check(b, b.o, b.lse)
 
 
-WEIGH = [s for s in ATTEND if s[5] <= 9000]
+WEIGH = [s for s in ATTEND if s[5] <= 9000 and s[0] != 24]
 
 
 @pytest.mark.parametrize("spec", WEIGH, ids=lambda s: "-".join(map(str, s[:6])) + "-" + s[7])
