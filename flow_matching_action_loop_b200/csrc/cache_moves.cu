@@ -151,16 +151,17 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
   }
   __syncthreads();
 
-  // radix select: after each digit, `left` of the keys that share the digits so far belong to the kept
+  // radix select: after each digit, `left` of the keys that share the digits so far belong to the kept;
+  // when those are all of them, the digits that follow do not matter
   uint32_t prefix = 0;
-  int left = keep;
+  int left = keep, shift = 32, last = 0;
   const int n32 = (n + 31) & ~31;
-  for (int p = 0; p < 4; ++p) {
-    const int shift = 24 - 8 * p;
-    uint32_t* hp = hist[p & 1];
+  for (bool all = false; !all && shift > 0; last ^= 1) {
+    shift -= 8;
+    uint32_t* hp = hist[last];
     for (int i = tid; i < n32; i += EV_THREADS) {   // whole warps
       const uint32_t k = i < n ? key[i] : 0u;
-      const bool in = i < n && (p == 0 || (k >> (shift + 8)) == prefix);
+      const bool in = i < n && (shift == 24 || (k >> (shift + 8)) == prefix);
       const uint32_t d = in ? (k >> shift) & 255u : 256u;
       const unsigned same = __match_any_sync(0xffffffffu, d);
       if (in && lane == __ffs(same) - 1) atomicAdd(&hp[d], static_cast<uint32_t>(__popc(same)));
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
       uint32_t t = 0;
       for (int r = 0; r < C; ++r) t += cl.map_shared_rank(hp, r)[tid];
       tot[tid] = t;
-      hist[(p + 1) & 1][tid] = 0;   // last read before this barrier, by every CTA
+      hist[last ^ 1][tid] = 0;   // last read before this barrier, by every CTA
     }
     __syncthreads();
     if (warp == 0) {   // lane l holds digits 255 - 8l .. 248 - 8l
@@ -197,11 +198,14 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
     __syncthreads();
     prefix = (prefix << 8) | static_cast<uint32_t>(s_digit);
     left = s_left;
+    all = tot[s_digit] == static_cast<uint32_t>(left);
   }
-  // keys above `prefix` are kept, and the first `left` of those equal to it, in slot order
+  last ^= 1;   // the last digit's histogram
+  // keys whose first digits are above `prefix` are kept, and the first `left` of those equal to it, in slot
+  // order
   if (tid == 0) {
     uint32_t e = 0;
-    for (int r = 0; r < c; ++r) e += cl.map_shared_rank(hist[1], r)[prefix & 255u];
+    for (int r = 0; r < c; ++r) e += cl.map_shared_rank(hist[last], r)[prefix & 255u];
     s_eq0 = static_cast<int>(e);
   }
   // each warp walks a contiguous part of the slice, so that ranks follow from ballots
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
   int cnt = 0;
   for (int i0 = wlo; i0 < whi; i0 += 32) {
     const int i = i0 + lane;
-    cnt += __popc(__ballot_sync(0xffffffffu, i < whi && key[i] == prefix));
+    cnt += __popc(__ballot_sync(0xffffffffu, i < whi && key[i] >> shift == prefix));
   }
   if (lane == 0) w_eq[warp] = cnt;
   __syncthreads();
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
     for (int i0 = wlo; i0 < whi; i0 += 32) {
       const int i = i0 + lane, slot = lo + i;
       const bool in = i < whi;
-      const uint32_t k = in ? key[i] : 0u;
+      const uint32_t k = in ? key[i] >> shift : 0u;
       const unsigned be = __ballot_sync(0xffffffffu, in && k == prefix);
       const bool kept = in && (k > prefix || (k == prefix && eq + __popc(be & below) < left));
       const bool hole = in && !kept && slot < keep, mover = kept && slot >= keep;
@@ -291,35 +295,30 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
       mv_src[tid] = s;
     }
     __syncthreads();
-    const int items = nb * 2 * nv;
+    // a warp moves U rows of K and V at a time, every load before the stores
     constexpr int U = 4;
-    for (int it0 = tid; it0 < items; it0 += EV_THREADS * U) {
-      uint4 x[U];
-      uint4* to[U];
+    for (int m0 = warp; m0 < nb; m0 += EV_WARPS * U) {
+      for (int e = lane; e < 2 * nv; e += 32) {
+        uint4* base = e < nv ? kr + e : vr + (e - nv);
+        uint4 x[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int it = it0 + u * EV_THREADS;
-        to[u] = nullptr;
-        if (it < items) {
-          const int m = it / (2 * nv), e = it - m * 2 * nv;
-          uint4* base = e < nv ? kr + e : vr + (e - nv);
-          x[u] = base[static_cast<size_t>(mv_src[m]) * nv];
-          to[u] = base + static_cast<size_t>(mv_dst[m]) * nv;
-        }
+        for (int u = 0; u < U; ++u)
+          if (m0 + u * EV_WARPS < nb) x[u] = base[static_cast<size_t>(mv_src[m0 + u * EV_WARPS]) * nv];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (m0 + u * EV_WARPS < nb) base[static_cast<size_t>(mv_dst[m0 + u * EV_WARPS]) * nv] = x[u];
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (to[u]) *to[u] = x[u];
     }
     __syncthreads();
   }
   cl.sync();   // no CTA leaves while another reads its lists
 }
 
-// CTAs per cluster: about 2048 slots a CTA.
-int evict_cluster(int S_max) {
+// CTAs per cluster: as many as give the GPU two CTAs per SM, of at least 128 slots, and what shared memory
+// asks for.
+int evict_cluster(int units, int S_max) {
   int C = 1;
-  while (C < EV_MAX_CLUSTER && S_max > C * 2048) C *= 2;
+  while (C < EV_MAX_CLUSTER && ((2 * C * units <= 296 && S_max >= 2 * C * 128) || S_max > C * 32768)) C *= 2;
   return C;
 }
 
@@ -339,7 +338,7 @@ cudaError_t launch_cache_commit(const MoveArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_cache_evict(const MoveArgs& a, cudaStream_t s) {
-  const int C = evict_cluster(a.S_max);
+  const int C = evict_cluster(a.B * a.Hkv, a.S_max);
   const int slice = ((a.S_max + C - 1) / C + 31) & ~31;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, a.Hkv, a.B);
