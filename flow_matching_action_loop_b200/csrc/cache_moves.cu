@@ -135,17 +135,25 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
   if (tid < 256) hist[0][tid] = 0;
   __syncthreads();
   int pm = INT32_MIN;
+#pragma unroll 4
   for (int i = tid; i < n; i += EV_THREADS) {
-    key[i] = rank_key(acc[lo + i]);
-    pm = max(pm, pos[lo + i]);
+    const float w = acc[lo + i];
+    const int q = pos[lo + i];
+    key[i] = rank_key(w);
+    pm = max(pm, q);
+    if (lo + i < keep) {   // as if it stayed; a freed slot's new token overwrites this
+      src[lo + i] = lo + i;
+      acc_out[lo + i] = w;
+      pos_out[lo + i] = q;
+    }
   }
   pm = __reduce_max_sync(0xffffffffu, pm);
   if (lane == 0) atomicMax(&pmax, pm);
   cl.sync();
   if (a.recent > 0) {
-    int last = INT32_MIN;
-    for (int r = 0; r < C; ++r) last = max(last, *cl.map_shared_rank(&pmax, r));
+    const int last = __reduce_max_sync(0xffffffffu, lane < C ? *cl.map_shared_rank(&pmax, lane) : INT32_MIN);
     const long long bound = static_cast<long long>(last) - a.recent;
+#pragma unroll 4
     for (int i = tid; i < n; i += EV_THREADS)
       if (pos[lo + i] > bound) key[i] = 0xffffffffu;
   }
@@ -163,12 +171,17 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
       const uint32_t k = i < n ? key[i] : 0u;
       const bool in = i < n && (shift == 24 || (k >> (shift + 8)) == prefix);
       const uint32_t d = in ? (k >> shift) & 255u : 256u;
-      const unsigned same = __match_any_sync(0xffffffffu, d);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&hp[d], static_cast<uint32_t>(__popc(same)));
+      if (shift == 24) {   // few digits (signs and exponents): one addition per digit and warp
+        const unsigned same = __match_any_sync(0xffffffffu, d);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&hp[d], static_cast<uint32_t>(__popc(same)));
+      } else if (in) {
+        atomicAdd(&hp[d], 1u);
+      }
     }
     cl.sync();
     if (tid < 256) {
       uint32_t t = 0;
+#pragma unroll 4
       for (int r = 0; r < C; ++r) t += cl.map_shared_rank(hp, r)[tid];
       tot[tid] = t;
       hist[last ^ 1][tid] = 0;   // last read before this barrier, by every CTA
@@ -203,10 +216,9 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
   last ^= 1;   // the last digit's histogram
   // keys whose first digits are above `prefix` are kept, and the first `left` of those equal to it, in slot
   // order
-  if (tid == 0) {
-    uint32_t e = 0;
-    for (int r = 0; r < c; ++r) e += cl.map_shared_rank(hist[last], r)[prefix & 255u];
-    s_eq0 = static_cast<int>(e);
+  if (warp == 0) {
+    const uint32_t e = lane < c ? cl.map_shared_rank(hist[last], lane)[prefix & 255u] : 0u;
+    s_eq0 = static_cast<int>(__reduce_add_sync(0xffffffffu, e));
   }
   // each warp walks a contiguous part of the slice, so that ranks follow from ballots
   const int part = ((n + EV_WARPS - 1) / EV_WARPS + 31) & ~31;
@@ -236,11 +248,6 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
       if (round == 1) {
         if (hole) list[nh + __popc(bh & below)] = static_cast<uint16_t>(i);
         if (mover) list[per - 1 - nm - __popc(bm & below)] = static_cast<uint16_t>(i);
-        if (kept && slot < keep) {
-          src[slot] = slot;
-          acc_out[slot] = acc[slot];
-          pos_out[slot] = pos[slot];
-        }
       }
       eq += __popc(be);
       nh += __popc(bh);
@@ -262,16 +269,19 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
     }
   }
   cl.sync();   // every CTA's lists and counts
-  if (tid == 0) {
-    int th = 0, tm = 0;
-    for (int r = 0; r < C; ++r) {
-      hole_base[r] = th;
-      move_base[r] = tm;
-      th += *cl.map_shared_rank(&n_hole, r);
-      tm += *cl.map_shared_rank(&n_move, r);
+  if (warp == 0) {   // C <= 16: sums over the CTAs before each
+    int th = lane < C ? *cl.map_shared_rank(&n_hole, lane) : 0;
+    int tm = lane < C ? *cl.map_shared_rank(&n_move, lane) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, th, o), z = __shfl_up_sync(0xffffffffu, tm, o);
+      if (lane >= o) th += y, tm += z;
     }
-    hole_base[C] = th;
-    move_base[C] = tm;
+    if (lane < C) {
+      hole_base[lane + 1] = th;
+      move_base[lane + 1] = tm;
+    }
+    if (lane == 0) hole_base[0] = move_base[0] = 0;
   }
   __syncthreads();
   const long long M = hole_base[C];
