@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
     }
     __syncthreads();
     // a warp moves U rows of K and V at a time, every load before the stores
-    constexpr int U = 4;
+    constexpr int U = 8;
     for (int m0 = warp; m0 < nb; m0 += EV_WARPS * U) {
       for (int e = lane; e < 2 * nv; e += 32) {
         uint4* base = e < nv ? kr + e : vr + (e - nv);
