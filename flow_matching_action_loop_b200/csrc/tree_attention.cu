@@ -9,6 +9,9 @@
 // so side by side over the same range of keys (with a range of its own for each, the tiles came from HBM
 // 2.6 times at 6 x 33000 slots and four row tiles).
 //
+// Where it costs few tiles more (launch_tree), a unit has a cluster of up to 16 CTAs instead, its tiles in
+// equal ranges, and the cluster joins its rows over distributed shared memory: no scratch, no second kernel.
+//
 // Inside a CTA, per tile t:
 //   copy warp     K(t+LA), V(t) by tensor map (128-byte swizzle) into a ring of shared-memory slots
 //   MMA warp      S(t+LA) = Q K^T, then O += P(t) V(t): tcgen05, fp32 in tensor memory; P is the A operand
@@ -26,6 +29,7 @@
 // P is rounded to bf16, the tensor core's operand type: half a bf16 step per weight, as much as the
 // rounding of o itself.
 #include <algorithm>
+#include <cooperative_groups.h>
 #include <type_traits>
 
 #include "fr.h"
@@ -45,6 +49,7 @@ constexpr int TA_REGS = 168, TA_REGS_SOFTMAX = 208, TA_REGS_OTHER = 88;
 static_assert(2 * TA_REGS_SOFTMAX + TA_REGS_OTHER == 3 * TA_REGS, "registers are only moved");
 constexpr int TA_CTAS = 148;                   // at most: the scratch holds two segments' rows for each
 constexpr float TA_RESCALE = 8.f;
+constexpr int TA_CLUSTER = 16;                 // CTAs of a cluster at most
 
 // Shared memory: QB query tiles, then NS ring slots of `piece` bytes.  At dh = 256 a K tile comes as two
 // pieces of 128 features, a V tile as two of 64 slots, so that the ring has five slots instead of two.
@@ -75,7 +80,35 @@ __device__ __forceinline__ void group_barrier(int g) { asm volatile("bar.sync %0
 __device__ __forceinline__ void ref_send(int w, int g) { asm volatile("bar.arrive %0, 64;" ::"r"(7 + 2 * w + g) : "memory"); }
 __device__ __forceinline__ void ref_wait(int w, int g) { asm volatile("bar.sync %0, 64;" ::"r"(7 + 2 * w + g) : "memory"); }
 
-template <int DH>
+// 16 features of a row joined over segments: O and the sum brought to the largest reference.
+struct MergedRow {
+  float m = -INFINITY, l = 0.f, x = 0.f, o[16] = {};
+  __device__ __forceinline__ void add(float m2, float l2, float x2, const float* v) {
+    const float mn = fmaxf(m, m2);
+    if (mn == -INFINITY) return;
+    const float w0 = exp2f(m - mn), w1 = exp2f(m2 - mn);
+    m = mn;
+    l = l * w0 + l2 * w1;
+    x += x2;   // NaN where a drafted value row was not finite
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = o[e] * w0 + v[e] * w1;
+  }
+  // Row rr of the group (head, token), features 16 fg on.
+  __device__ __forceinline__ void store(const TreeArgs& a, int b, int hk, int rr, int fg, int dh) const {
+    const int tok = rr % a.N, hq = hk * (a.Hq / a.Hkv) + rr / a.N;
+    const float inv = (l == 0.f ? 0.f : 1.f / l) + x;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+    st_global_32(a.o + ((static_cast<size_t>(b) * a.N + tok) * a.Hq + hq) * dh + fg * 16, w);
+    if (a.lse && fg == 0)
+      a.lse[(static_cast<size_t>(b) * a.Hq + hq) * a.N + tok] =
+          m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
+};
+
+// CL: one cluster per unit.
+template <int DH, bool CL>
 __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_constant__ TreeArgs a) {
   using G = TreeGeom<DH>;
   extern __shared__ __align__(1024) uint8_t dsm[];
@@ -145,11 +178,26 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
       fence_mbar_init();
     }
     __syncwarp();
-    const TileRange r = tile_range(a, a.Hkv * NB, grp);
+    TileRange r = {};
+    if constexpr (!CL) r = tile_range(a, a.Hkv * NB, grp);
     if ((tid & 31) == 0) {
       TileIter it;
-      it.start(a, r, a.Hkv * NB);
-      any_seg = it.next(a, RT, NB, r_in);
+      if constexpr (CL) {   // the unit's tiles in equal ranges; no further segment
+        const int unit = blockIdx.x / a.cluster, c = blockIdx.x - unit * a.cluster;
+        it = {};
+        it.rt = unit % RT;
+        it.hk = unit / RT % a.Hkv;
+        it.b = unit / (RT * a.Hkv);
+        it.len = a.lens[it.b];
+        it.nb = tiles_of(a, it.len);
+        it.tile0 = it.nb * c / a.cluster;
+        it.tile1 = it.nb * (c + 1) / a.cluster;
+        any_seg = it.tile0 < it.tile1;
+        if (it.nb == 0 && it.len >= 0 && c + it.rt + it.hk == 0) report_sample(a.status, CACHE_BAD_LEN, it.b);
+      } else {
+        it.start(a, r, a.Hkv * NB);
+        any_seg = it.next(a, RT, NB, r_in);
+      }
       if (any_seg) {
         load_q(it);
         load_k(it, it.tile0);
@@ -162,7 +210,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
     tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
   }
-  grid_dep_launch();   // the merge kernel waits for this whole grid before it reads
+  if constexpr (!CL) grid_dep_launch();   // the merge kernel waits for this whole grid before it reads
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -493,14 +541,16 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         const float at = ref == -INFINITY ? 0.f : ref;
         const float lt = fabsf(l0) * exp2f(r0 - at) + fabsf(l1) * exp2f(r1 - at);
         const float bad_v = signbit(l0) || signbit(l1) ? NAN : 0.f;
-        const bool whole = it.tile1 - it.tile0 == it.nb;
+        const bool whole = !CL && it.tile1 - it.tile0 == it.nb;
         const bool mine = row < Rv && ok;
         const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) + bad_v : 1.f;
         __nv_bfloat16* orow = a.o + (static_cast<size_t>(it.b) * a.N + tok) * a.Hq * DH + static_cast<size_t>(hq) * DH;
         // a partial segment's rows: [dh / 4][rows][4] floats, then (reference, sum, spoilt) [rows][4], so
         // that a warp's rows leave side by side
-        const int RW = min(128, R);
-        float* part = a.scratch + static_cast<size_t>(2 * blockIdx.x + (it.tile0 > 0 ? 0 : 1)) * RW * OLD + 4 * row;
+        // (a cluster's in this CTA's shared memory, whose tiles have all been used)
+        const int RW = CL ? 128 : min(128, R);
+        float* part = CL ? reinterpret_cast<float*>(dsm) + 4 * row
+                         : a.scratch + static_cast<size_t>(2 * blockIdx.x + (it.tile0 > 0 ? 0 : 1)) * RW * OLD + 4 * row;
 #pragma unroll 1
         for (int c0 = hh * (DH / 2); c0 < (hh + 1) * (DH / 2); c0 += 32) {
           uint32_t ov[32];
@@ -545,6 +595,38 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }
+  if constexpr (CL) {
+    // ---------------- the cluster's rows: 16 features of a row a thread, over the CTAs that had tiles
+    namespace cg = cooperative_groups;
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    const TileIter u = first_seg;
+    const int C = a.cluster, Rv = min(128, R - u.rt * 128), n = min(C, u.nb);
+    const int me = static_cast<int>(cl.block_rank());
+    for (int i = me * TA_THREADS + tid; u.nb > 0 && i < Rv * (DH / 16); i += C * TA_THREADS) {
+      const int fg = i / Rv, row = i - fg * Rv;
+      MergedRow m;
+      constexpr int UN = 2;   // CTAs in flight (88 registers: the copy/MMA warpgroup's)
+      for (int k0 = 0; k0 < n; k0 += UN) {
+        float4 v[UN][4], st[UN];
+#pragma unroll
+        for (int k = 0; k < UN; ++k)
+          if (k0 + k < n) {
+            // the CTA that has tile floor(nb (k0 + k) / n): with nb < C some have none
+            const int c = u.nb >= C ? k0 + k : ((k0 + k + 1) * C - 1) / u.nb;
+            const float* p = cl.map_shared_rank(reinterpret_cast<const float*>(dsm), c) + 4 * row;
+            st[k] = *reinterpret_cast<const float4*>(p + (DH / 4) * 128 * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[k][e] = *reinterpret_cast<const float4*>(p + (fg * 4 + e) * 128 * 4);
+          }
+#pragma unroll
+        for (int k = 0; k < UN; ++k)
+          if (k0 + k < n) m.add(st[k].x, st[k].y, st[k].z, reinterpret_cast<const float*>(v[k]));
+      }
+      m.store(a, u.b, u.hk, u.rt * 128 + row, fg, DH);
+    }
+    cl.sync();   // no CTA leaves while another reads its rows
+  }
 }
 
 // ------------------------------------------------------------------ merge
@@ -584,19 +666,7 @@ __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant
   if (c0 == c1) return;   // one segment: written by k_tree_attn
   // a CTA's rows that begin a unit are in its second slot, those that go on with one in its first
   auto slot_of = [&](int c) { return 2 * (c * a.rtg + rt % a.rtg) + (c == c0 ? 1 : 0); };
-  float m = -INFINITY, l = 0.f, x = 0.f, o[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) o[e] = 0.f;
-  auto add = [&](float m2, float l2, float x2, const float* v) {
-    const float mn = fmaxf(m, m2);
-    if (mn == -INFINITY) return;
-    const float w0 = exp2f(m - mn), w1 = exp2f(m2 - mn);
-    m = mn;
-    l = l * w0 + l2 * w1;
-    x += x2;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = o[e] * w0 + v[e] * w1;
-  };
+  MergedRow m;
   if (row < Rv) {
     constexpr int UN = 4;   // segments in flight
     for (int cb = c0 + sub; cb <= c1; cb += UN * split) {
@@ -613,29 +683,21 @@ __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant
       }
 #pragma unroll
       for (int i = 0; i < UN; ++i)
-        if (cb + i * split <= c1) add(st[i].x, st[i].y, st[i].z, reinterpret_cast<const float*>(v[i]));
+        if (cb + i * split <= c1) m.add(st[i].x, st[i].y, st[i].z, reinterpret_cast<const float*>(v[i]));
     }
   }
   if (split > 1) {
-    red[tid][0] = m;
+    red[tid][0] = m.m;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) red[tid][e + 1] = o[e];
-    red_l[tid] = l;
-    red_x[tid] = x;
+    for (int e = 0; e < 16; ++e) red[tid][e + 1] = m.o[e];
+    red_l[tid] = m.l;
+    red_x[tid] = m.x;
     __syncthreads();
     if (sub == 0)
-      for (int w = tid + rows * FG; w < TM_THREADS; w += rows * FG) add(red[w][0], red_l[w], red_x[w], &red[w][1]);
+      for (int w = tid + rows * FG; w < TM_THREADS; w += rows * FG) m.add(red[w][0], red_l[w], red_x[w], &red[w][1]);
   }
   if (row >= Rv || sub != 0) return;
-  const int rr = rt * 128 + row, tok = rr % a.N, hq = hk * g + rr / a.N;
-  const float inv = (l == 0.f ? 0.f : 1.f / l) + x;
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
-  st_global_32(a.o + (static_cast<size_t>(b) * a.N + tok) * a.Hq * DH + static_cast<size_t>(hq) * DH + fg * 16, w);
-  if (a.lse && fg == 0)
-    a.lse[(static_cast<size_t>(b) * a.Hq + hq) * a.N + tok] =
-        m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  m.store(a, b, hk, rt * 128 + row, fg, DH);
 }
 
 // CTAs per group: all of a unit's row tiles up to 16; of more, the batch size from 8 to 16 that leaves the
@@ -659,7 +721,22 @@ cudaError_t launch_tree(TreeArgs& a, cudaStream_t s) {
       !encode_rows_map(&a.tm_k, a.k, DH, a.S_max, a.S_max, planes, TREE_KEYS, G::k_blocks) ||
       !encode_rows_map(&a.tm_v, a.v, DH, a.S_max, a.S_max, planes, G::v_keys, DH / 64))
     return cudaErrorInvalidValue;
-  k_tree_attn<DH><<<a.groups * a.rtg, TA_THREADS, G::smem, s>>>(a);
+  if (a.cluster > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(planes) * RT * a.cluster);
+    cfg.blockDim = dim3(TA_THREADS);
+    cfg.dynamicSmemBytes = G::smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = a.cluster;
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_tree_attn<DH, true>, a);
+  }
+  k_tree_attn<DH, false><<<a.groups * a.rtg, TA_THREADS, G::smem, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.S_max <= TREE_KEYS) return e;   // a unit of one tile is never split
   // segments per unit if every sample is as long as can be
@@ -679,9 +756,44 @@ cudaError_t launch_tree(TreeArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k_tree_merge<DH>, a, split);
 }
 
+// Clusters of c CTAs that can be resident together, per head dim (64, 128, 256), on each device.
+constexpr int MAX_DEVICES = 64;
+int g_clusters[MAX_DEVICES][3][TA_CLUSTER + 1];
+
 template <int DH>
-cudaError_t tree_init() {
-  return cudaFuncSetAttribute(k_tree_attn<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeGeom<DH>::smem);
+cudaError_t tree_init(int* clusters) {
+  const auto smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(k_tree_attn<DH, false>, smem, TreeGeom<DH>::smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_tree_attn<DH, true>, smem, TreeGeom<DH>::smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_tree_attn<DH, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (int c = 2; e == cudaSuccess && c <= TA_CLUSTER; ++c) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(TA_THREADS);
+    cfg.dynamicSmemBytes = TreeGeom<DH>::smem;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = c;
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&clusters[c], k_tree_attn<DH, true>, &cfg);
+  }
+  return e;
+}
+
+// CTAs of a unit's cluster, or 1: tiles shared over the whole GPU.  A cluster is taken if all of them are
+// resident together and the longest sample's share per CTA is at most CLUSTER_EXTRA tiles above an equal
+// share of all tiles over the GPU: a tile takes about 0.6 us there, the merge kernel and a CTA's second
+// segment 4 us and more.
+constexpr int CLUSTER_EXTRA = 5;
+int tree_cluster(const int* resident, int ctas, int64_t units, int tiles) {
+  int best = 1;
+  for (int c = 2; c <= TA_CLUSTER && c <= tiles; ++c)
+    if (units <= resident[c] && ((tiles + c - 1) / c < (tiles + best - 1) / best)) best = c;
+  const int64_t share = units * tiles / ctas;
+  return best > 1 && (tiles + best - 1) / best <= share + CLUSTER_EXTRA ? best : 1;
 }
 
 }  // namespace
@@ -697,14 +809,21 @@ cudaError_t launch_tree_attention(const TreeArgs& args, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  tree_groups(std::min(nsm, TA_CTAS), (a.Hq / a.Hkv * a.N + 127) / 128, a.rtg, a.groups);
+  const int RT = (a.Hq / a.Hkv * a.N + 127) / 128, ctas = std::min(nsm, TA_CTAS);
+  tree_groups(ctas, RT, a.rtg, a.groups);
+  a.cluster = 1;
+  if (dev < MAX_DEVICES)
+    a.cluster = tree_cluster(g_clusters[dev][a.dh == 64 ? 0 : a.dh == 128 ? 1 : 2], ctas,
+                             static_cast<int64_t>(a.B) * a.Hkv * RT, (a.S_max + TREE_KEYS - 1) / TREE_KEYS);
   return a.dh == 64 ? launch_tree<64>(a, s) : a.dh == 128 ? launch_tree<128>(a, s) : launch_tree<256>(a, s);
 }
 
 cudaError_t cache_ops_init() {
-  cudaError_t e;
-  if ((e = tree_init<64>()) != cudaSuccess || (e = tree_init<128>()) != cudaSuccess ||
-      (e = tree_init<256>()) != cudaSuccess)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev >= MAX_DEVICES) return e;
+  if ((e = tree_init<64>(g_clusters[dev][0])) != cudaSuccess || (e = tree_init<128>(g_clusters[dev][1])) != cudaSuccess ||
+      (e = tree_init<256>(g_clusters[dev][2])) != cudaSuccess)
     return e;
   if ((e = weights_init()) != cudaSuccess) return e;
   return cache_moves_init();
