@@ -422,3 +422,100 @@ def test_pointers_of_the_host_are_refused():
         with pytest.raises(fr.FrError) as e:
             fr.fr_attention_tree(ptr(q), ptr(k), ptr(d), ptr(lens), 0, ptr(d), 0, 1, 1, 1, 1, 8, 64, 0, 0, stream())
         assert e.value.code == fr.FR_ERR_ARG and "current device" in str(e.value)
+
+
+class _Device:
+    """A handle's device buffer as a torch tensor, without a copy."""
+
+    def __init__(self, address, shape, typestr):
+        self.__cuda_array_interface__ = {"data": (address, False), "shape": tuple(shape), "typestr": typestr, "version": 3}
+
+
+def test_a_run_together_on_a_handles_cache():
+    """Prefix pass, then two rounds on one layer of its KV cache: draft, attend, accept, weigh, commit, evict.
+    Every step against its definition on the state that the step before left."""
+    import synthetic
+    cfg = synthetic.PrefixConfig("run", L=2, D=256, Hq=4, Hkv=2, dh=64, F=512, B=2, P=150, dtype="bf16")
+    inp = synthetic.make_prefix_pass_inputs(cfg, seed=4)
+    room = 230                                     # the handle's largest prefix: room behind this one's 150 tokens
+    backbone = fr.PrefixPass(cfg, P_max=room)
+    backbone.load_weights(inp["weights"])
+    backbone.run(torch.from_numpy(inp["emb"]).bfloat16().cuda())
+    assert backbone.sync_status() == 0
+    address_k, nbytes = backbone.buffer("kv_k")
+    address_v, _ = backbone.buffer("kv_v")
+    layer_bytes = nbytes // cfg.L
+    S = room + 1                                   # slots per (sample, KV head) of this handle
+    assert layer_bytes // (cfg.B * cfg.Hkv * cfg.dh * 2) == S
+    shape, layer = (cfg.B, cfg.Hkv, S, cfg.dh), 1
+    k = torch.as_tensor(_Device(address_k + layer * layer_bytes, shape, "<i2"), device="cuda").view(torch.bfloat16)
+    v = torch.as_tensor(_Device(address_v + layer * layer_bytes, shape, "<i2"), device="cuda").view(torch.bfloat16)
+    assert k.data_ptr() == address_k + layer * layer_bytes
+    got_k, _ = backbone.read_kv(layer, 1, 150)
+    assert np.array_equal(k[1, :, :150].contiguous().view(torch.int16).cpu().numpy().view(np.uint16), got_k)
+
+    rng, g = np.random.default_rng(0), torch.Generator().manual_seed(0)
+    B, Hq, Hkv, dh, N, keep, recent = cfg.B, cfg.Hq, cfg.Hkv, cfg.dh, 13, 120, 16
+    acc, acc2 = torch.zeros(B, Hkv, S).cuda(), torch.zeros(B, Hkv, S).cuda()
+    pos = torch.arange(S, dtype=torch.int32).expand(B, Hkv, S).contiguous().cuda()
+    pos2 = torch.zeros_like(pos)
+    lens, lens2 = torch.tensor([150, 150], dtype=torch.int32).cuda(), torch.zeros(2, dtype=torch.int32).cuda()
+    src = torch.zeros(B, Hkv, keep, dtype=torch.int32).cuda()
+    for step in range(2):
+        n = lens.tolist()
+        words = np.stack([fr.fr_tree_mask([int(rng.integers(-1, i)) if i else -1 for i in range(N)]) for _ in range(B)])
+        d_words = torch.from_numpy(words.view(np.int32)).cuda()
+        for b in range(B):   # the drafts' rows and positions
+            k[b, :, n[b]:n[b] + N] = torch.randn(Hkv, N, dh, generator=g).bfloat16().cuda()
+            v[b, :, n[b]:n[b] + N] = torch.randn(Hkv, N, dh, generator=g).bfloat16().cuda()
+            pos[b, :, n[b]:n[b] + N] = 1000 * (step + 1) + torch.arange(N, dtype=torch.int32).cuda()
+        c = Case.__new__(Case)
+        c.B, c.Hq, c.Hkv, c.dh, c.N, c.S, c.lens, c.words = B, Hq, Hkv, dh, N, S, n, words
+        c.q = (torch.randn(B, Hq, N, dh, generator=g) * 1.5).bfloat16()
+        c.k, c.v = k.cpu(), v.cpu()
+        c.device()
+        fr.fr_attention_tree(ptr(c.dq), ptr(k), ptr(v), ptr(lens), ptr(d_words), ptr(c.o), ptr(c.lse), B, Hq, Hkv, N, S, dh,
+                             ptr(c.scratch), c.nscratch, stream())
+        oracle = c.oracle()
+        check(c, c.o, c.lse, oracle)
+
+        path = np.zeros((B, N), np.int32)   # the accepted branch: the deepest token's ancestors
+        npath = np.zeros(B, np.int32)
+        use = np.zeros((B, 1), np.uint32)
+        for b in range(B):
+            best = max(range(N), key=lambda i: bin(int(words[b, i, 0])).count("1"))
+            nodes = [j for j in range(N) if (int(words[b, best, 0]) >> j) & 1]
+            npath[b] = len(nodes)
+            path[b, :len(nodes)] = nodes
+            use[b, 0] = words[b, best, 0]
+        d_use, d_path, d_np = (torch.from_numpy(x).cuda() for x in (use.view(np.int32), path, npath))
+        before, lse = acc.cpu().numpy(), c.lse.double().cpu().numpy()
+        fr.fr_attention_weights(ptr(c.dq), ptr(k), ptr(c.lse), ptr(lens), ptr(d_words), ptr(d_use), ptr(acc), B, Hq, Hkv, N, S,
+                                dh, stream())
+        want, _ = R.weigh(c.q.double().numpy(), c.k.double().numpy(), lse, n, words, use, before)
+        for b in range(B):
+            m = n[b] + N
+            assert np.all(np.abs(acc[b, :, :m].cpu().numpy() - want[b, :, :m]) <= 2.0 ** -13 * want[b, :, :m] + 1e-30)
+
+        fr.fr_cache_commit(ptr(k), ptr(v), ptr(acc), ptr(pos), ptr(lens), ptr(d_path), ptr(d_np), ptr(lens2), B, Hkv, N, S, dh,
+                           fr.FR_DTYPE_BF16, stream())
+        lens, lens2 = lens2, lens
+        assert lens.tolist() == [x + int(y) for x, y in zip(n, npath)]
+        for b in range(B):
+            at = torch.from_numpy(n[b] + path[b, :npath[b]].astype(np.int64))
+            assert torch.equal(k[b, :, n[b]:n[b] + npath[b]].cpu(), c.k[b][:, at])
+        state = [x.clone() for x in (k, v, acc, pos)]
+        fr.fr_cache_evict(ptr(k), ptr(v), ptr(acc), ptr(pos), ptr(lens), ptr(acc2), ptr(pos2), ptr(lens2), ptr(src), B, Hkv, S,
+                          dh, fr.FR_DTYPE_BF16, keep, recent, stream())
+        m = lens.tolist()
+        assert lens2.tolist() == [min(x, keep) for x in m]
+        for b in range(B):
+            for h in range(Hkv):
+                at = R.evict_one(state[2][b, h, :m[b]].cpu().numpy(), state[3][b, h, :m[b]].cpu().numpy(), keep, recent)
+                t = torch.from_numpy(at).cuda()
+                assert src[b, h, :len(at)].tolist() == at.tolist()
+                for new, old in zip((k, v, acc2, pos2), state):
+                    assert torch.equal(new[b, h, :len(at)], old[b, h][t])
+        acc, acc2, pos, pos2, lens, lens2 = acc2, acc, pos2, pos, lens2, lens
+    assert fr.fr_ops_sync_status(stream()) == 0
+    backbone.close()
