@@ -274,16 +274,15 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
                 w2[1] = add_f32x2(w2[1], pack_f32x2(ex2_approx(y.x), ex2_approx(y.y)));
               }
             };
-            uint32_t s0[32], s1[32];
-            tmem_ld32_nowait(ts, s0);
-            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {   // 32 columns at a time, the next ones on their way
-              if (32 * i < cols) {
-                uint32_t* now = i & 1 ? s1 : s0;
-                if (32 * (i + 1) < cols) tmem_ld32_nowait(ts + 32 * (i + 1), i & 1 ? s0 : s1);
-                sum32(now, 32 * i, vis[i]);
+            for (int i = 0; i < 2; ++i) {   // 64 columns at a time
+              if (64 * i < cols) {
+                uint32_t sc[64];
+                tmem_ld32_nowait(ts + 64 * i, sc);
+                if (64 * i + 32 < cols) tmem_ld32_nowait(ts + 64 * i + 32, sc + 32);
                 tmem_wait_ld();
+                sum32(sc, 64 * i, vis[2 * i]);
+                if (64 * i + 32 < cols) sum32(sc + 32, 64 * i + 32, vis[2 * i + 1]);
               }
             }
             tc_fence_before();

@@ -9,7 +9,7 @@
 // so side by side over the same range of keys (with a range of its own for each, the tiles came from HBM
 // 2.6 times at 6 x 33000 slots and four row tiles).
 //
-// Where it costs few tiles more (launch_tree), a unit has a cluster of up to 16 CTAs instead, its tiles in
+// Where it costs few tiles more (tree_cluster), a unit has a cluster of up to 16 CTAs instead, its tiles in
 // equal ranges, and the cluster joins its rows over distributed shared memory: no scratch, no second kernel.
 //
 // Inside a CTA, per tile t:
@@ -19,7 +19,7 @@
 //   softmax warps two groups of four take the tiles in turn, a thread a row: maximum and sum in fp32,
 //                 P = 2^(s - ref)
 // One group's loads, maxima and stores thus overlap the other's exponentials (with both groups on one tile,
-// half a row each, the multi-function unit idled half of a tile's 2500 cycles).  The groups hand the row's
+// half a row each, the multi-function unit idled more than half of a tile's 2500 cycles).  The groups hand the row's
 // reference on from tile to tile.  Two score buffers (LA = 2) let both groups have a tile; at dh = 256
 // tensor memory has room for one (LA = 1), and S(t+1) is issued once the scores of tile t are in registers.
 // P has columns of its own: with P in those of the scores, S(t+1) waited for P(t-1) V(t-1) as well (1.97 us a
@@ -66,7 +66,7 @@ struct TreeGeom {
   static constexpr int k_blocks = DH / 64 / pieces;             // feature blocks per K piece
 };
 
-// 32 bytes, a whole sector, to a 16-byte aligned address that is a multiple of 32 past o's rows.
+// 32 bytes, a whole sector, to a 32-byte aligned address.
 __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
                "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
           // finite, and the rows past the drafts in the last step of 16 slots that the product takes, are
           // zeroed where they landed.
           const int pv = G::pieces * (2 * t + G::LA + 1);    // ring position of V(t)
-          // (a slot's phase can be told only once its use before is known to have landed: it was V(t - 1)'s at most)
+          // (its slots' uses before have landed once P(t - 1) V(t - 1) is done: only then do their phases tell)
           if (t > 0) wait(&bar_o[(t - 1) & 1], ((t - 1) >> 1) & 1);
           for (int p = 0; p < G::pieces; ++p) wait(&full[(pv + p) % G::NS], ((pv + p) / G::NS) & 1);
           constexpr int CPR = DH / 8;                        // 16-byte words per row
@@ -536,6 +536,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         sum_sh[hh][row] = spoilt ? -l : l;
         ref_sh[hh][row] = ref;
         pair_barrier(pw);
+        tc_fence_after();   // (the other group's wait for the last product may be the one that counts)
         const float l0 = sum_sh[0][row], l1 = sum_sh[1][row], r0 = ref_sh[0][row], r1 = ref_sh[1][row];
         ref = fmaxf(r0, r1);
         const float at = ref == -INFINITY ? 0.f : ref;
