@@ -173,6 +173,137 @@ def test_tree_attention_hidden_values_do_not_leak():
     check(c, c.o, c.lse, oracle)
 
 
+@pytest.mark.parametrize("dh", [64, 128, 256])
+def test_tree_attention_hidden_values_in_a_large_batch(dh):
+    """The same in every third sample of a batch that is shared over the whole GPU."""
+    B, N = 60, 20
+    c = Case(B, 8, 4, dh, N, 700, [20 + 11 * b for b in range(B)], "chain")
+    seen = np.tril(np.ones((N, N), bool))
+    seen[:, 7] = False
+    seen[7, 7] = True
+    c.words = np.stack([R.words_of(seen)] * B)
+    oracle = c.oracle()
+    for b in range(0, B, 3):
+        c.k[b, :, c.lens[b] + 7] = float("inf")
+        c.v[b, 1:, c.lens[b] + 7, 5] = float("nan")
+        c.v[b, 0, c.lens[b] + 7] = float("-inf")
+    c.device().run()
+    o = c.o.view(B, N, 8, dh)
+    for b in range(0, B, 3):
+        assert torch.isnan(o[b, 7]).all()
+        o[b, 7] = torch.from_numpy(oracle[0][b, 7]).cuda().bfloat16()
+        c.lse[b, :, 7] = torch.from_numpy(oracle[2][b, :, 7]).cuda().float()
+    check(c, c.o, c.lse, oracle)
+
+
+@pytest.mark.parametrize("dh", [64, 128, 256])
+def test_tree_attention_large_scores_over_the_whole_gpu(dh):
+    c = Case(20, 8, 8, dh, 3, 3000, [2900 - 7 * b for b in range(20)], "tree", seed=5, scale=5.0)
+    for b in range(20):
+        c.k[b, :, :c.lens[b]] *= torch.linspace(0.02, 3.0, c.lens[b])[None, :, None].to(torch.bfloat16)
+    c.device().run()
+    check(c, c.o, c.lse)
+
+
+def test_tree_attention_in_a_cache_far_longer_than_its_sequences():
+    c = Case(3, 8, 2, 128, 5, 60000, [100, 0, 700], "tree").device()
+    c.run()
+    check(c, c.o, c.lse)
+
+
+def test_offsets_past_four_gigabytes():
+    """K and V of 4.6 GB each: only the last sample, whose rows lie past 2^32 bytes, is in use."""
+    B, Hq, Hkv, dh, N, S = 9, 16, 8, 64, 6, 520000
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    assert (B * Hkv - 1) * S * dh * 2 > 1 << 32
+    c = Case(1, Hq, Hkv, dh, N, 400, [390], "tree")
+    k, v = torch.empty(B, Hkv, S, dh, dtype=torch.bfloat16, device="cuda"), torch.empty(B, Hkv, S, dh, dtype=torch.bfloat16, device="cuda")
+    k[-1, :, :400], v[-1, :, :400] = c.k[0].cuda(), c.v[0].cuda()
+    lens = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    lens[-1] = 390
+    q = torch.zeros(B, Hq, N, dh, dtype=torch.bfloat16, device="cuda")
+    q[-1] = c.q[0].cuda()
+    words = torch.zeros(B, N, 1, dtype=torch.int32, device="cuda")
+    words[-1] = torch.from_numpy(c.words[0].view(np.int32)).cuda()
+    o, lse = torch.empty(B, N, Hq * dh, dtype=torch.bfloat16, device="cuda"), torch.empty(B, Hq, N, device="cuda")
+    n = fr.fr_attention_tree_scratch_bytes(B, Hq, Hkv, N, S, dh)
+    scratch = torch.empty(n, dtype=torch.uint8, device="cuda")
+    fr.fr_attention_tree(ptr(q), ptr(k), ptr(v), ptr(lens), ptr(words), ptr(o), ptr(lse), B, Hq, Hkv, N, S, dh, ptr(scratch), n, stream())
+    check(c, o[-1:], lse[-1:])
+    acc, pos = torch.zeros(B, Hkv, S, device="cuda"), torch.zeros(B, Hkv, S, dtype=torch.int32, device="cuda")
+    fr.fr_attention_weights(ptr(q), ptr(k), ptr(lse), ptr(lens), ptr(words), 0, ptr(acc), B, Hq, Hkv, N, S, dh, stream())
+    want, _ = R.weigh(c.q.double().numpy(), c.k.double().numpy(), lse[-1:].double().cpu().numpy(), [390], c.words, None, np.zeros((1, Hkv, S)))
+    assert np.all(np.abs(acc[-1].cpu().numpy() - want[0])[:, :396] <= 2.0 ** -13 * want[0][:, :396]) and float(acc[:-1].abs().max()) == 0.0
+    path, npath = torch.zeros(B, N, dtype=torch.int32, device="cuda"), torch.full((B,), 3, dtype=torch.int32, device="cuda")
+    path[-1] = torch.tensor([1, 2, 5, 0, 0, 0], dtype=torch.int32)
+    lens2, lens3 = torch.empty_like(lens), torch.empty_like(lens)
+    kk, vv = k[-1, :, :396].clone(), v[-1, :, :396].clone()
+    fr.fr_cache_commit(ptr(k), ptr(v), 0, 0, ptr(lens), ptr(path), ptr(npath), ptr(lens2), B, Hkv, N, S, dh, fr.FR_DTYPE_BF16, stream())
+    at = [391, 392, 395]
+    assert lens2.tolist() == [-1] * (B - 1) + [393]
+    assert torch.equal(k[-1, :, 390:393], kk[:, at]) and torch.equal(v[-1, :, 390:393], vv[:, at])
+    kk, vv = k[-1, :, :393].clone(), v[-1, :, :393].clone()
+    acc2, pos2, src = torch.zeros_like(acc), torch.zeros_like(pos), torch.zeros(B, Hkv, 100, dtype=torch.int32, device="cuda")
+    fr.fr_cache_evict(ptr(k), ptr(v), ptr(acc), ptr(pos), ptr(lens2), ptr(acc2), ptr(pos2), ptr(lens3), ptr(src), B, Hkv, S, dh,
+                      fr.FR_DTYPE_BF16, 100, 0, stream())
+    assert lens3.tolist() == [-1] * (B - 1) + [100]
+    for h in range(Hkv):
+        at = R.evict_one(acc[-1, h, :393].cpu().numpy(), np.zeros(393, np.int32), 100, 0)
+        assert src[-1, h].tolist() == at.tolist()
+        t = torch.from_numpy(at).cuda()
+        assert torch.equal(k[-1, h, :100], kk[h][t]) and torch.equal(v[-1, h, :100], vv[h][t])
+    assert fr.fr_ops_sync_status(stream()) == 0
+
+
+def test_the_four_ops_in_one_graph_over_the_whole_gpu():
+    """Captured together at sizes that take the merge kernel; replayed on another state."""
+    B, Hq, Hkv, dh, N, S, keep = 40, 16, 8, 128, 5, 900, 500
+    a = Case(B, Hq, Hkv, dh, N, S, [890 - 20 * b for b in range(B)], "tree")
+    b = Case(B, Hq, Hkv, dh, N, S, [95 + 20 * b for b in range(B)], "tree", seed=1)
+    lens2, lens3 = torch.zeros(B, dtype=torch.int32).cuda(), torch.zeros(B, dtype=torch.int32).cuda()
+    acc, acc2 = torch.zeros(B, Hkv, S).cuda(), torch.zeros(B, Hkv, S).cuda()
+    pos = torch.arange(S, dtype=torch.int32).expand(B, Hkv, S).contiguous().cuda()
+    pos2, src = torch.zeros_like(pos), torch.zeros(B, Hkv, keep, dtype=torch.int32).cuda()
+    path = torch.tensor([0, 2, 3, 4, 4], dtype=torch.int32).expand(B, N).contiguous().cuda()
+    npath = torch.tensor([i % 5 for i in range(B)], dtype=torch.int32).cuda()
+    a.device(), b.device()
+
+    def ops(c, s):
+        fr.fr_attention_tree(ptr(c.dq), ptr(c.dk), ptr(c.dv), ptr(c.dlens), ptr(c.dwords), ptr(c.o), ptr(c.lse), B, Hq, Hkv, N, S,
+                             dh, ptr(c.scratch), c.nscratch, s)
+        fr.fr_attention_weights(ptr(c.dq), ptr(c.dk), ptr(c.lse), ptr(c.dlens), ptr(c.dwords), 0, ptr(acc), B, Hq, Hkv, N, S, dh, s)
+        fr.fr_cache_commit(ptr(c.dk), ptr(c.dv), ptr(acc), ptr(pos), ptr(c.dlens), ptr(path), ptr(npath), ptr(lens2), B, Hkv, N, S,
+                           dh, fr.FR_DTYPE_BF16, s)
+        fr.fr_cache_evict(ptr(c.dk), ptr(c.dv), ptr(acc), ptr(pos), ptr(lens2), ptr(acc2), ptr(pos2), ptr(lens3), ptr(src), B, Hkv,
+                          S, dh, fr.FR_DTYPE_BF16, keep, 8, s)
+
+    def reset(c):
+        c.dk.copy_(c.k), c.dv.copy_(c.v)
+        acc.zero_(), acc2.zero_(), pos2.zero_(), src.zero_()
+        pos.copy_(torch.arange(S, dtype=torch.int32).expand(B, Hkv, S))
+
+    ops(b, stream())   # the answer of the plain calls on b's state
+    want = [x.clone() for x in (b.o, b.lse, b.dk, b.dv, acc, pos, lens2, acc2, pos2, lens3, src)]
+    check(b, b.o, b.lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    reset(a)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        ops(a, torch.cuda.current_stream().cuda_stream)
+    graph.replay()
+    check(a, a.o, a.lse)
+    a.k, a.v = b.k, b.v
+    a.dq.copy_(b.dq), a.dlens.copy_(b.dlens), a.dwords.copy_(b.dwords)
+    for _ in range(2):
+        reset(a)
+        graph.replay()
+        for x, y in zip((a.o, a.lse, a.dk, a.dv, acc, pos, lens2, acc2, pos2, lens3, src), want):
+            assert torch.equal(torch.nan_to_num(x.float()), torch.nan_to_num(y.float()))
+    assert fr.fr_ops_sync_status(stream()) == 0
+
+
 def test_tree_attention_refuses_bad_lengths_on_the_device():
     c = Case(4, 4, 2, 64, 3, 100, [50, 97, 20, 4], "tree").device()
     c.dlens[0], c.dlens[2] = 98, 2 ** 31 - 1      # lens + N past the cache
