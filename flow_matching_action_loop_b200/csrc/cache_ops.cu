@@ -37,6 +37,13 @@ int check_tree_sizes(const char* op, int B, int Hq, int Hkv, int N, int S_max, i
               FR_TREE_MAX_NODES, FR_CACHE_MAX_SLOTS);
     return FR_ERR_UNSUPPORTED;
   }
+  // key tiles of all samples, KV heads and (at most) row tiles: the kernels count them in an int
+  const int64_t line = static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(Hq / Hkv) * N + 127) / 128) *
+                       ((static_cast<int64_t>(S_max) + 127) / 128);
+  if (line > INT32_MAX) {
+    set_error("%s: a cache this long is not served at this batch and number of heads", op);
+    return FR_ERR_UNSUPPORTED;
+  }
   if (N > S_max) {
     set_error("%s: %d drafted tokens do not fit a cache of %d slots", op, N, S_max);
     return FR_ERR_SHAPE;
@@ -88,9 +95,7 @@ int fr_tree_mask(const int32_t* parents, int n, uint32_t* mask) {
 }
 
 size_t fr_attention_tree_scratch_bytes(int B, int Hq, int Hkv, int N, int S_max, int dh) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || N < 1 || S_max < N || Hq % Hkv != 0 || (dh != 64 && dh != 128 && dh != 256) ||
-      N > FR_TREE_MAX_NODES || S_max > FR_CACHE_MAX_SLOTS || B > 4096 || Hq > 1024)
-    return 0;
+  if (check_tree_sizes("fr_attention_tree_scratch_bytes", B, Hq, Hkv, N, S_max, dh)) return 0;
   return tc::tree_scratch_bytes(B, Hq, Hkv, N, S_max, dh);
 }
 

@@ -411,19 +411,19 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         }
         __syncwarp();
         if ((tid & 31) == 0) mbar_arrive(&bar_l[t & 1]);
-        auto weights = [&](auto which) {   // P of half a row
-          constexpr int half = decltype(which)::value;
+        auto weights = [&](auto which) {   // P of a quarter of a row
+          constexpr int q = decltype(which)::value;
           const uint64_t off2 = pack_f32x2(-off, -off);
-          uint32_t pk[32];
+          uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 64; e += 2) {
+          for (int e = 0; e < 32; e += 2) {
             const float2 x = unpack_f32x2(fma_f32x2(
-                pack_f32x2(__uint_as_float(s[64 * half + e]), __uint_as_float(s[64 * half + e + 1])), sl22, off2));
+                pack_f32x2(__uint_as_float(s[32 * q + e]), __uint_as_float(s[32 * q + e + 1])), sl22, off2));
             const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
             ps[(e >> 1) & 1] = add_f32x2(ps[(e >> 1) & 1], pack_f32x2(p0, p1));
             pk[e >> 1] = pack_bf16x2(p0, p1);
           }
-          tmem_st32(tp + 32 * half, pk);
+          tmem_st16(tp + 16 * q, pk);
         };
         if (work) {
           if (boundary) {
@@ -460,6 +460,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         if (work) {
           weights(std::integral_constant<int, 0>{});
           weights(std::integral_constant<int, 1>{});
+          weights(std::integral_constant<int, 2>{});
+          weights(std::integral_constant<int, 3>{});
           const float2 pt = unpack_f32x2(add_f32x2(ps[0], ps[1]));
           l += pt.x + pt.y;
           if (tile > it.tile0 && __any_sync(0xffffffffu, corr != 1.f)) {
@@ -481,25 +483,29 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
           // zeroed where they landed.
           const int pv = G::pieces * (2 * t + G::LA + 1);    // ring position of V(t)
           // (its slots' uses before have landed once P(t - 1) V(t - 1) is done: only then do their phases tell)
-          if (t > 0) wait(&bar_o[(t - 1) & 1], ((t - 1) >> 1) & 1);
+          if (G::pieces == 2 && t > 0) wait(&bar_o[(t - 1) & 1], ((t - 1) >> 1) & 1);
           for (int p = 0; p < G::pieces; ++p) wait(&full[(pv + p) % G::NS], ((pv + p) / G::NS) & 1);
-          constexpr int CPR = DH / 8;                        // 16-byte words per row
-          auto word = [&](int r, int c) {
-            const int vp = r / G::v_keys;
-            return reinterpret_cast<uint4*>(ring + ((pv + vp) % G::NS) * G::piece + (c >> 3) * (G::v_keys * 128) +
-                                            (r - vp * G::v_keys) * 128 + (c & 7) * 16);
+          // a thread has one 16-byte column of every 128 / (dh / 8)-th row
+          constexpr int CPR = DH / 8, step = 128 / CPR;
+          const int c16 = row % CPR;
+          uint8_t* vp[G::pieces];
+#pragma unroll
+          for (int p = 0; p < G::pieces; ++p)
+            vp[p] = ring + ((pv + p) % G::NS) * G::piece + (c16 >> 3) * (G::v_keys * 128) + (c16 & 7) * 16;
+          auto word = [&](int r) {
+            return reinterpret_cast<uint4*>(r < G::v_keys ? vp[0] + r * 128 : vp[G::pieces - 1] + (r - G::v_keys) * 128);
           };
           uint32_t(&bd)[4] = bad[hh][nbound % 3];
-          const int r0 = max(0, len - key0), items = (min(TREE_KEYS, (keys - key0 + 15) & ~15) - r0) * CPR;
+          const int r_first = max(0, len - key0) + row / CPR, r_end = min(TREE_KEYS, (keys - key0 + 15) & ~15);
           if (ok)
 #pragma unroll 4
-            for (int i = row; i < items; i += 128) {
-              const int r = r0 + i / CPR;
-              uint4* x = word(r, i % CPR);
+            for (int r = r_first; r < r_end; r += step) {
+              uint4* x = word(r);
+              const uint4 y = *x;
               if (key0 + r >= keys) {
                 *x = make_uint4(0, 0, 0, 0);
               } else {
-                const uint4 y = *x;
+                // a bf16 is not finite if its exponent's bits are all ones
                 const uint32_t w[4] = {y.x, y.y, y.z, y.w};
                 bool odd = false;
 #pragma unroll
@@ -514,10 +520,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
           for (int i = 0; i < 4; ++i) odd4[i] = bd[i];
           if (odd4[0] | odd4[1] | odd4[2] | odd4[3]) {
             if (ok)
-              for (int i = row; i < items; i += 128) {
-                const int r = r0 + i / CPR;
-                if ((bd[r >> 5] >> (r & 31)) & 1u) *word(r, i % CPR) = make_uint4(0, 0, 0, 0);
-              }
+              for (int r = r_first; r < r_end; r += step)
+                if ((bd[r >> 5] >> (r & 31)) & 1u) *word(r) = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) spoilt |= (vis[i] & odd4[i]) != 0;
           }
@@ -638,7 +642,7 @@ constexpr int TM_THREADS = 256;
 template <int DH>
 __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant__ TreeArgs a, int split) {
   constexpr int OLD = DH + 4, FG = DH / 16;   // feature groups
-  __shared__ long long sh_T, sh_cum;
+  __shared__ int sh_T, sh_cum;
   __shared__ float red[TM_THREADS][17];       // reference, 16 features (one split's threads after the other's)
   __shared__ float red_l[TM_THREADS], red_x[TM_THREADS];
   const int g = a.Hq / a.Hkv, R = g * a.N, RT = (R + 127) >> 7, NB = (RT + a.rtg - 1) / a.rtg;
@@ -649,20 +653,20 @@ __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant
   const int Rv = min(128, R - rt * 128), RW = min(128, R);
   const int sub = tid / (rows * FG), fg = tid / rows % FG, row = blockIdx.x * rows + tid % rows;
   if (warp == 0) {
-    const long long T = tiles_before(a, U, a.B);
+    const int T = tiles_before(a, U, a.B);
     if (lane == 0) sh_T = T;
   } else if (warp == 1) {
-    const long long c = tiles_before(a, U, b);
+    const int c = tiles_before(a, U, b);
     if (lane == 0) sh_cum = c;
   }
   const int nb = sample_tiles(a, b);
   __syncthreads();
   grid_dep_wait();
   if (nb == 0 || blockIdx.x * rows >= Rv) return;
-  const long long T = sh_T, t0 = sh_cum + static_cast<long long>(hk * NB + rt / a.rtg) * nb;
+  const int T = sh_T, t0 = sh_cum + (hk * NB + rt / a.rtg) * nb;
   // group c < n holds tiles [T c / n, T (c + 1) / n), at least one
-  const int n = static_cast<int>(min(T, static_cast<long long>(a.groups)));
-  auto holder = [&](long long t) { return static_cast<int>(div_long((t + 1) * n - 1, T)); };
+  const int n = min(T, a.groups);
+  auto holder = [&](int t) { return static_cast<int>((static_cast<long long>(t + 1) * n - 1) / T); };
   const int c0 = holder(t0), c1 = holder(t0 + nb - 1);
   if (c0 == c1) return;   // one segment: written by k_tree_attn
   // a CTA's rows that begin a unit are in its second slot, those that go on with one in its first

@@ -22,9 +22,10 @@ __device__ __forceinline__ void report_sample(unsigned* status, uint32_t where, 
 // The line of tiles: the samples' units one after the other, a unit's tiles in a row.  A unit is a KV head
 // and a batch of up to a.rtg row tiles (the weights kernel: all rows).  The line is cut into equal ranges,
 // one per group of a.rtg CTAs; CTA r of a group runs row tile r of each batch, so that a group reads a key
-// tile from HBM once and from the L2 after that.
+// tile from HBM once and from the L2 after that.  (The entry points refuse sizes whose line is longer than an
+// int.)
 struct TileRange {
-  long long t0, t1, cum;   // this group's tiles; first tile of sample b
+  int t0, t1, cum;   // this group's tiles; first tile of sample b
   int b, len;              // sample of t0
 };
 
@@ -36,7 +37,7 @@ __device__ __forceinline__ int tiles_of(const TreeArgs& a, int len) {
 __device__ __forceinline__ int sample_tiles(const TreeArgs& a, int b) { return tiles_of(a, a.lens[b]); }
 
 struct TileIter {
-  long long t, t1, cum;
+  int t, t1, cum;
   int b, len, nb, U;
   int hk, rt, tile0, tile1;   // segment: tiles [tile0, tile1) of the nb of unit (b, hk), row tile rt
   __device__ __forceinline__ void start(const TreeArgs& a, const TileRange& r, int U_) {
@@ -52,65 +53,57 @@ struct TileIter {
   __device__ __forceinline__ bool next(const TreeArgs& a, int RT, int NB, int r) {
     do {
       if (t >= t1) return false;
-      while (t - cum >= static_cast<long long>(U) * nb) {
-        cum += static_cast<long long>(U) * nb;
+      while (t - cum >= U * nb) {
+        cum += U * nb;
         len = a.lens[++b];
         nb = tiles_of(a, len);
       }
-      const int rel = static_cast<int>(t - cum), u = rel / nb;
+      const int rel = t - cum, u = rel / nb;
       hk = NB == 1 ? u : u / NB;
       rt = (u - hk * NB) * a.rtg + r;
       tile0 = rel - u * nb;
-      tile1 = static_cast<int>(min(static_cast<long long>(nb), tile0 + (t1 - t)));
+      tile1 = min(nb, tile0 + (t1 - t));
       t += tile1 - tile0;
     } while (rt >= RT);   // the last batch has fewer row tiles
     return true;
   }
 };
 
-__device__ __forceinline__ unsigned long long div_long(unsigned long long x, unsigned long long y) {
-  return (x | y) >> 32 ? x / y : static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-}
 // First tile of CTA c of n: floor(T c / n).
-__device__ __forceinline__ long long share_begin(long long T, int c, int n) {
-  const long long q = div_long(T, n);
-  return q * c + static_cast<int>(T - q * n) * c / n;
+__device__ __forceinline__ int share_begin(int T, int c, int n) {
+  const int q = T / n;
+  return q * c + (T - q * n) * c / n;
 }
 
 // One warp: the tiles of the samples before b_end.
-__device__ __forceinline__ long long tiles_before(const TreeArgs& a, int U, int b_end) {
-  long long sum = 0;
+__device__ __forceinline__ int tiles_before(const TreeArgs& a, int U, int b_end) {
+  int sum = 0;
   for (int b = threadIdx.x & 31; b < b_end; b += 32) sum += sample_tiles(a, b);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * U;
+  return __reduce_add_sync(0xffffffffu, sum) * U;
 }
 
 // One warp: group c's share of the line.  The first min(T, groups) groups have at least one tile each.
 // CTA 0 reports the samples of a bad length.
 __device__ __forceinline__ TileRange tile_range(const TreeArgs& a, int U, int c) {
   const int lane = threadIdx.x & 31;
-  long long T = 0;
+  int T = 0;
   for (int b = lane; b < a.B; b += 32) {
     const int len = a.lens[b], n = tiles_of(a, len);
     if (blockIdx.x == 0 && n == 0 && len >= 0) report_sample(a.status, CACHE_BAD_LEN, b);
     T += n;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
-  T *= U;
-  const int n = static_cast<int>(min(T, static_cast<long long>(a.groups)));
+  T = __reduce_add_sync(0xffffffffu, T) * U;
+  const int n = min(T, a.groups);
   TileRange r = {0, 0, 0, 0, -1};
   if (c >= n) return r;
   r.t0 = share_begin(T, c, n);
   r.t1 = share_begin(T, c + 1, n);
   for (int b0 = 0; b0 < a.B; b0 += 32) {   // the sample that holds t0
-    const int len = b0 + lane < a.B ? a.lens[b0 + lane] : -1;
-    const long long own = static_cast<long long>(tiles_of(a, len)) * U;
-    long long incl = own;
+    const int len = b0 + lane < a.B ? a.lens[b0 + lane] : -1, own = tiles_of(a, len) * U;
+    int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, r.cum + incl > r.t0);
