@@ -7,13 +7,14 @@
 //
 // The 128-slot tiles of all (sample, KV head) pairs form one line, cut into equal ranges over the CTAs (one
 // per SM).  A CTA keeps up to 256 of the pair's rows in shared memory and streams its K tiles past them
-// (from the second 256 rows on out of the L2); a slot's sum is added to acc by the same thread each time.
+// (from the second 256 rows on out of the L2); a slot's sum is added to acc by one thread in each pass.
 //   copy warp      query rows, K tiles by tensor map (128-byte swizzle) into a ring
 //   MMA warp       K(t) Q^T, 128 rows at a time, into one of a sum group's two score buffers in tensor memory
 //   sum warps      two groups of four take the tiles in turn, a thread a slot: 2^(s - lse) in fp32.  (With
 //                  both groups on one tile, half of the columns each, a tile's exponentials had nothing to
 //                  overlap with: 1870 cycles for 128 x 128 scores against 1024 of the exponentials.)
 #include <algorithm>
+#include <type_traits>
 
 #include "fr.h"
 #include "tree_device.h"
@@ -48,6 +49,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
   __shared__ int abort_flag;
   __shared__ TileRange range;
   __shared__ __align__(16) float lse_sh[AW_PASS];   // -lse in log2 units, -inf: a row that gives nothing
+  __shared__ uint32_t live_sh[AW_PASS / 32];        // 0 bits: such rows of the pass, whose q may hold anything
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = a.Hq / a.Hkv, R = g * a.N;
   const int passes = (R + AW_PASS - 1) / AW_PASS;
@@ -210,6 +212,8 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
             if (counts && v != -INFINITY) x = -v * 1.4426950408889634f;
           }
           lse_sh[tid] = x;
+          const unsigned live = __ballot_sync(0xffffffffu, x != -INFINITY || tid >= rows);   // (q reads as 0 past the rows)
+          if (lane == 0) live_sh[warp] = live;
         }
         asm volatile("bar.sync 5, 256;" ::: "memory");
         // a committed slot adds to its sum, a drafted one begins with the first rows; fetched a tile ahead
@@ -236,9 +240,6 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
                 const uint32_t* words = a.mask ? a.mask + (static_cast<size_t>(it.b) * a.N + n) * a.W : nullptr;
                 vis[i] = seen_slots(words, n, a.N, a.W, tile * TREE_KEYS + 32 * pw - len);
               }
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (ls[32 * i + lane] == -INFINITY) vis[i] = 0;
               auto stage = [&](int st, uint32_t m) {   // the four words side by side: a shuffle waits long
                 uint32_t y[4];
 #pragma unroll
@@ -253,26 +254,36 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
               stage(2, 0x33333333u);
               stage(1, 0x55555555u);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vis[i] &= live_sh[4 * c + i];
             if (!__all_sync(0xffffffffu, mbar_test(&bar_s[buf], (item >> 1) & 1)) && ok)
               ok = __all_sync(0xffffffffu, mbar_wait(&bar_s[buf], (item >> 1) & 1, WAIT_LIMIT_NS) && !*abort_v);
             tc_fence_after();
             const uint32_t ts = tS + buf * AW_CHUNK + lanes;
-            auto sum32 = [&](uint32_t* s, int col, uint32_t v) {
-              if (boundary) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((v >> e) & 1u)) s[e] = 0xff800000u;   // -inf
-              }
+            // all: every column counts, for every slot
+            auto terms = [&](const uint32_t* s, int col, uint32_t v, auto all) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
                 const float4 l4 = *reinterpret_cast<const float4*>(ls + col + e);
-                const float2 x = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl22,
-                                                        pack_f32x2(l4.x, l4.y)));
-                const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), sl22,
-                                                        pack_f32x2(l4.z, l4.w)));
+                float2 x = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl22,
+                                                  pack_f32x2(l4.x, l4.y)));
+                float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), sl22,
+                                                  pack_f32x2(l4.z, l4.w)));
+                if constexpr (!decltype(all)::value) {   // whatever score and lse are
+                  if (!((v >> e) & 1u)) x.x = -INFINITY;
+                  if (!((v >> (e + 1)) & 1u)) x.y = -INFINITY;
+                  if (!((v >> (e + 2)) & 1u)) y.x = -INFINITY;
+                  if (!((v >> (e + 3)) & 1u)) y.y = -INFINITY;
+                }
                 w2[0] = add_f32x2(w2[0], pack_f32x2(ex2_approx(x.x), ex2_approx(x.y)));
                 w2[1] = add_f32x2(w2[1], pack_f32x2(ex2_approx(y.x), ex2_approx(y.y)));
               }
+            };
+            auto sum32 = [&](const uint32_t* s, int col, uint32_t v) {
+              if (__all_sync(0xffffffffu, v == 0xffffffffu))
+                terms(s, col, v, std::true_type());
+              else
+                terms(s, col, v, std::false_type());
             };
 #pragma unroll
             for (int i = 0; i < 2; ++i) {   // 64 columns at a time

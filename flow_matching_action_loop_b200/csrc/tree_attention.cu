@@ -85,11 +85,14 @@ struct MergedRow {
   float m = -INFINITY, l = 0.f, x = 0.f, o[16] = {};
   __device__ __forceinline__ void add(float m2, float l2, float x2, const float* v) {
     const float mn = fmaxf(m, m2);
-    if (mn == -INFINITY) return;
+    x += x2;   // NaN where a drafted value row was not finite
+    if (mn == -INFINITY) {   // no score above -inf: the sums are 0, or NaN with the scores
+      l += l2;
+      return;
+    }
     const float w0 = exp2f(m - mn), w1 = exp2f(m2 - mn);
     m = mn;
     l = l * w0 + l2 * w1;
-    x += x2;   // NaN where a drafted value row was not finite
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[e] = o[e] * w0 + v[e] * w1;
   }
@@ -103,7 +106,7 @@ struct MergedRow {
     st_global_32(a.o + ((static_cast<size_t>(b) * a.N + tok) * a.Hq + hq) * dh + fg * 16, w);
     if (a.lse && fg == 0)
       a.lse[(static_cast<size_t>(b) * a.Hq + hq) * a.N + tok] =
-          m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+          l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
 };
 
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
             *reinterpret_cast<float4*>(part + static_cast<size_t>(DH / 4) * RW * 4) = make_float4(ref, lt, bad_v, 0.f);
           } else if (a.lse) {
             a.lse[(static_cast<size_t>(it.b) * a.Hq + hq) * a.N + tok] =
-                ref == -INFINITY ? -INFINITY : (ref + log2f(lt)) * 0.6931471805599453f;
+                lt == 0.f ? -INFINITY : (ref + log2f(lt)) * 0.6931471805599453f;
           }
         }
         tc_fence_before();

@@ -287,7 +287,7 @@ int fr_set_wait_limit(fr_handle* h, uint64_t limit_ns);
 /* ---- device bounds checks (checked builds) ---- */
 
 /* 1 if this library was built with device bounds checks (-DFR_DEVICE_CHECKS), else 0.  In a checked
- * build every store of the GEMM epilogues, of the attention kernels and of the persistent kernel
+ * build every store of the GEMM epilogues, of fr_attention's kernels and of the persistent kernel
  * verifies its index against its buffer's extent; an index at or past it latches FR_ERR_DEVICE in the
  * status word (fr_sync_status / fr_ops_sync_status: where-code and index) and the store is skipped.
  * No counterpart in the pages: it stands in for a memory checker in debugging. */
@@ -504,9 +504,9 @@ int fr_attention_noalloc(const void* q, const void* k, const void* v, void* o, i
  * Common to the four:
  *   - lens is device int32 [B], so a captured graph follows the sequences' growth.  lens[b] < 0 marks a
  *     padded sample: nothing of it is read or written (its lens_out is its lens).
- *   - Kernel-side checks: a sample whose lens[b] (or path, npath) is out of range is skipped, its outputs
- *     stay as they were, and the fault is latched for fr_ops_sync_status (FR_ERR_DEVICE, the message
- *     gives the where-code 0xc0.. and the sample).
+ *   - Kernel-side checks, in every build: a sample whose lens[b] (or path, npath) is out of range is
+ *     skipped, its outputs stay as they were (its lens_out is its lens), and the fault is latched for
+ *     fr_ops_sync_status (FR_ERR_DEVICE, the message gives the where-code 0xc0.. and the sample).
  *   - They run on the current device, on `stream`; every pointer must be memory of that device (checked).
  *     q, k, v and scratch must be 16-byte aligned, o 32-byte, the others 4-byte aligned; outputs
  *     must not overlap inputs.  They allocate nothing and can be captured into graphs (make a first call
@@ -538,10 +538,11 @@ int fr_tree_mask(const int32_t* parents, int n, uint32_t* mask);
  * sees drafted tokens 0..i (N = 1 is the decoding of single tokens).  o: bf16 [B][N][Hq*dh] (the layout of
  * fr_attention); lse: float32 [B][Hq][N], or NULL.  A row that sees no key has o = 0 and lse = -inf.
  * What a token does not see cannot reach its row, whatever it holds; a drafted value row that holds a NaN
- * or an infinity makes the whole o row of the tokens that see it NaN.
+ * or an infinity makes the whole o row of the tokens that see it NaN.  A NaN among the scores that a row
+ * sees makes its o and lse NaN.
  * scratch: fr_attention_tree_scratch_bytes() bytes (NULL when that is 0; 40 MiB cover every size).
  * Limits: dh in {64, 128, 256}, Hq % Hkv == 0, N <= FR_TREE_MAX_NODES, S_max <= FR_CACHE_MAX_SLOTS,
- * B <= 4096, Hq <= 1024.
+ * B <= 4096, Hq <= 1024, and B * Hkv * ceil(Hq / Hkv * N / 128) * ceil(S_max / 128) < 2^31.
  */
 int fr_attention_tree(const void* q, const void* k, const void* v, const int32_t* lens, const uint32_t* mask,
                       void* o, float* lse, int B, int Hq, int Hkv, int N, int S_max, int dh, void* scratch,
@@ -556,7 +557,8 @@ size_t fr_attention_tree_scratch_bytes(int B, int Hq, int Hkv, int N, int S_max,
  * the rows that see slot s.  acc float32 [B][Hkv][S_max]: committed slots acc[s] += w[s], drafted slots
  * acc[s] = w[s]; later slots stay as they were.  q, k, lens, mask as fr_attention_tree had them, lse as it
  * left them (a row of lse = -inf gives nothing); use: [B][ceil(N/32)] words, bit i set when token i
- * counts (say, was accepted), or NULL: all.  Limits: those of fr_attention_tree.
+ * counts (say, was accepted), or NULL: all.  Rows that give nothing may hold anything in q.
+ * Limits: those of fr_attention_tree.
  */
 int fr_attention_weights(const void* q, const void* k, const float* lse, const int32_t* lens, const uint32_t* mask,
                          const uint32_t* use, float* acc, int B, int Hq, int Hkv, int N, int S_max, int dh,
@@ -578,7 +580,8 @@ int fr_cache_commit(void* k, void* v, float* acc, int32_t* pos, const int32_t* l
 /*
  * fr_cache_evict -- trim each sample to `keep` committed tokens, in each KV head those of largest acc.
  * Before all others come the tokens of the last `recent` positions: pos > (largest pos of the sample's head)
- * - recent.  Equal acc: the lowest slot first; a NaN ranks lowest.  Kept tokens below slot `keep` stay; the
+ * - recent (should equal positions make more than `keep` of them: the lowest slots).  Equal acc: the lowest
+ * slot first; a NaN ranks lowest.  Kept tokens below slot `keep` stay; the
  * others move into the freed slots below `keep`, in ascending order of both (attention over committed
  * tokens does not depend on their order).  acc_out, pos_out [B][Hkv][S_max] and src int32 [B][Hkv][keep]
  * receive, per slot j < min(lens[b], keep), the token's acc, pos and old slot; src is -1 after them, and

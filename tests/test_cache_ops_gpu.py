@@ -8,6 +8,8 @@ summed in float32 is off by at most dh * 2^-24 * sum|q_d k_d| (delta after the s
   o    2^-8 |o| for the rounding of the output and 2^-8 sum p|v| for that of each p to bf16 (half a bf16
        step each), and sum p|v| * 2 * (lse's tolerance) for the relative error of each p;
   acc  w * (lse's tolerance + rows * 2^-24) for the weights' sum, 2^-23 of the result for the last add.
+Where the ops run on each other's results, 2^-13 of the weight covers this: at dh = 64 sum|q_d k_d| / 8 is below
+24, so that delta < 64 * 24 * 2^-24 < 2^-13.4, and the other terms are below 2^-16 together.
 Slots past the drafted tokens hold NaN in every test, and outputs that must stay as they were a marker.
 """
 import numpy as np
@@ -194,6 +196,54 @@ def test_tree_attention_hidden_values_in_a_large_batch(dh):
         o[b, 7] = torch.from_numpy(oracle[0][b, 7]).cuda().bfloat16()
         c.lse[b, :, 7] = torch.from_numpy(oracle[2][b, :, 7]).cuda().float()
     check(c, c.o, c.lse, oracle)
+
+
+# a unit alone, split over a cluster, over CTAs of many units, of several row tiles
+@pytest.mark.parametrize("spec", [(1, 4, 2, 64, 5, 100, [60]), (2, 8, 1, 256, 7, 3000, [2900, 2500]), (1, 2, 1, 128, 130, 5000, [4700]),
+                                  (40, 4, 4, 128, 5, 900, [880 - 7 * b for b in range(40)])], ids=lambda s: "-".join(map(str, s[:6])))
+def test_a_query_that_is_not_finite_spoils_its_own_row_alone(spec):
+    c = Case(*spec, "tree").device()
+    c.run()
+    o, lse = c.o.clone().view(c.B, c.N, c.Hq, c.dh), c.lse.clone()
+    at = [(0, 0, 0), (c.B - 1, c.Hq - 1, c.N - 1), (0, c.Hq // 2, c.N // 2)]
+    for b, h, i in at:
+        c.dq[b, h, i] = float("nan")
+    c.run()
+    o2 = c.o.view(o.shape)
+    rest = torch.ones(c.B, c.Hq, c.N, dtype=torch.bool, device="cuda")
+    for b, h, i in at:
+        assert torch.isnan(o2[b, i, h]).all() and torch.isnan(c.lse[b, h, i])
+        rest[b, h, i] = False
+    assert torch.equal(o2.transpose(1, 2)[rest], o.transpose(1, 2)[rest]) and torch.equal(c.lse[rest], lse[rest])
+
+
+@pytest.mark.parametrize("dh", [64, 128, 256])
+def test_weights_of_rows_that_are_not_finite(dh):
+    """Rows out of use may hold anything; a NaN row reaches the slots that it sees, no others."""
+    B, Hq, Hkv, N, S, lens = 2, 80, 2, 9, 700, [600, 77]
+    c = Case(B, Hq, Hkv, dh, N, S, lens, "tree").device()
+    _, _, lse, _ = c.oracle()
+    use = np.full((B, 1), 0x1ff & ~0x24, np.uint32)     # tokens 2 and 5 do not count
+    d_use, d_lse = torch.from_numpy(use.view(np.int32)).cuda(), torch.from_numpy(lse).float().cuda()
+
+    def weights():
+        acc = torch.zeros(B, Hkv, S, device="cuda")
+        fr.fr_attention_weights(ptr(c.dq), ptr(c.dk), ptr(d_lse), ptr(c.dlens), ptr(c.dwords), ptr(d_use), ptr(acc), B, Hq, Hkv, N, S,
+                                dh, stream())
+        return acc
+
+    want = weights()
+    for v in (float("nan"), float("inf")):
+        c.dq[:, ::3, 2], c.dq[:, :, 5] = v, -v
+        d_lse[:, ::3, 2], d_lse[:, ::2, 5] = float("nan"), v
+        assert torch.equal(weights(), want)
+    d_lse[1, 7, 3] = float("nan")                       # a row in use, of sample 1 and KV head 0
+    got = weights()
+    sees = np.concatenate([np.ones(lens[1], bool), R.sees(c.words[1], N)[3]])
+    n = lens[1] + N
+    assert torch.equal(torch.isnan(got[1, 0, :n]).cpu(), torch.from_numpy(sees))
+    got[1, 0, :n][torch.from_numpy(sees).cuda()] = want[1, 0, :n][torch.from_numpy(sees).cuda()]
+    assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("dh", [64, 128, 256])

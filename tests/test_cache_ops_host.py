@@ -42,7 +42,9 @@ def test_tree_mask_refusals(abi):
 SIZES = [((0, 8, 1, 4, 100, 128), "ARG"), ((1, 0, 1, 4, 100, 128), "ARG"), ((1, 8, 0, 4, 100, 128), "ARG"), ((1, 8, 1, 0, 100, 128), "ARG"),
          ((1, 8, 1, 4, 0, 128), "ARG"), ((1, 8, 1, 4, 100, -1), "ARG"), ((1, 8, 3, 4, 100, 128), "UNSUPPORTED"),
          ((1, 8, 1, 4, 100, 96), "UNSUPPORTED"), ((1, 8, 1, 257, 1000, 128), "UNSUPPORTED"), ((1, 8, 1, 4, (1 << 24) + 1, 128), "UNSUPPORTED"),
-         ((4097, 8, 1, 4, 100, 128), "UNSUPPORTED"), ((1, 1025, 1, 4, 100, 128), "UNSUPPORTED"), ((1, 8, 1, 4, 3, 128), "SHAPE")]
+         ((4097, 8, 1, 4, 100, 128), "UNSUPPORTED"), ((1, 1025, 1, 4, 100, 128), "UNSUPPORTED"), ((1, 8, 1, 4, 3, 128), "SHAPE"),
+         # 4096 samples x 2048 row tiles x 257 key tiles: more than an int counts
+         ((4096, 1024, 1, 256, 257 * 128, 64), "UNSUPPORTED"), ((4096, 1024, 1, 256, 1 << 24, 64), "UNSUPPORTED")]
 
 
 @pytest.mark.parametrize("sizes,code", SIZES)
