@@ -13,6 +13,10 @@
 //   sum warps      two groups of four take the tiles in turn, a thread a slot: 2^(s - lse) in fp32.  (With
 //                  both groups on one tile, half of the columns each, a tile's exponentials had nothing to
 //                  overlap with: 1870 cycles for 128 x 128 scores against 1024 of the exponentials.)
+//
+// Single tokens of 32 samples with up to 8191 slots, 8 KV heads of 128: 59 us, 338 MB at 5.7 TB/s (memory).  Trees of
+// 63 tokens over 6 x 32767 slots, 8 query heads of 256: 49 us, 1005 TFLOP/s, the multi-function unit and the tensor
+// pipe each half busy.
 #include <algorithm>
 #include <type_traits>
 

@@ -15,7 +15,8 @@ namespace cg = cooperative_groups;
 // ------------------------------------------------------------------ commit
 // One CTA per (K or V, KV head, sample).  path ascends, so row i moves down (path[i] >= i) and no later
 // source lies below a written row: rows go in rounds of what the CTA holds in registers, every load of a
-// round before its stores, one barrier between them.
+// round before its stores, one barrier between them.  64 samples, 8 heads of 128 features, up to 63 rows each: 5.5 us
+// on the device for 16 MB (2.9 TB/s, mostly launch and two dependent loads); a call's host time is twice that.
 constexpr int CM_THREADS = 256;
 constexpr int CM_VECS = 8;   // 16-byte words a thread holds per round
 
@@ -78,6 +79,12 @@ __global__ void __launch_bounds__(CM_THREADS) k_cache_commit(const __grid_consta
 // order, its freed slots below `keep` (holes) and its kept slots at or past it (movers), both of which
 // have the same number over the cluster.  The r-th hole takes the r-th mover: only those rows of K and V
 // move, and as no hole is a mover the copies need no order.
+//
+// At 16 samples of up to 16384 slots, 8 heads of 128 bf16 features, trimmed to 12001: 80 us, of it 25 us selection
+// and 45 us moves of 256-byte rows (119 MB written, as many read, 5.3 TB/s), which the memory bounds.
+// Two CTAs of 512 threads per KV head and sample there; four took 87 us, four of 256 threads 84 us, two of 1024
+// 100 us, one 133 us.  One head of 866 slots trimmed to 512: 10.2 us, a chain of cluster barriers (1 us each
+// with the reads behind it).
 constexpr int EV_THREADS = 512, EV_WARPS = EV_THREADS / 32;
 constexpr int EV_MAX_CLUSTER = 16;
 constexpr int EV_SLICE_BYTES = 6;   // per slot of a slice: key (4) + list entry (2)
@@ -89,11 +96,11 @@ __device__ __forceinline__ uint32_t rank_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constant__ MoveArgs a) {
+__global__ void __launch_bounds__(EV_THREADS, 2) k_cache_evict(const __grid_constant__ MoveArgs a) {
   extern __shared__ __align__(16) uint8_t ev_dyn[];
   __shared__ uint32_t hist[2][256], tot[256];
-  __shared__ int pmax, n_hole, n_move, s_digit, s_left, s_eq0;
-  __shared__ int w_eq[EV_WARPS], w_hole[EV_WARPS], w_move[EV_WARPS];
+  __shared__ int pmax, n_hole, n_move, s_digit, s_left, s_tied;
+  __shared__ int w_eq[EV_WARPS], w_events[EV_WARPS];
   __shared__ int hole_base[EV_MAX_CLUSTER + 1], move_base[EV_MAX_CLUSTER + 1];
   __shared__ int mv_dst[EV_THREADS], mv_src[EV_THREADS];
   cg::cluster_group cl = cg::this_cluster();
@@ -135,49 +142,57 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
   if (tid < 256) hist[0][tid] = 0;
   __syncthreads();
   int pm = INT32_MIN;
+  const int n32 = (n + 31) & ~31;
 #pragma unroll 4
-  for (int i = tid; i < n; i += EV_THREADS) {
-    const float w = acc[lo + i];
-    const int q = pos[lo + i];
-    key[i] = rank_key(w);
+  for (int i = tid; i < n32; i += EV_THREADS) {   // whole warps
+    const bool in = i < n;
+    const float w = in ? acc[lo + i] : 0.f;
+    const int q = in ? pos[lo + i] : INT32_MIN;
+    const uint32_t k = rank_key(w), d = in ? k >> 24 : 256u;
+    // the first digit's histogram: few digits (signs and exponents), one addition per digit and warp
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    if (in && lane == __ffs(same) - 1) atomicAdd(&hist[0][d], static_cast<uint32_t>(__popc(same)));
     pm = max(pm, q);
-    if (lo + i < keep) {   // as if it stayed; a freed slot's new token overwrites this
+    if (in) key[i] = k;
+    if (in && lo + i < keep) {   // as if it stayed; a freed slot's new token overwrites this
       src[lo + i] = lo + i;
       acc_out[lo + i] = w;
       pos_out[lo + i] = q;
     }
   }
-  pm = __reduce_max_sync(0xffffffffu, pm);
-  if (lane == 0) atomicMax(&pmax, pm);
-  cl.sync();
   if (a.recent > 0) {
-    const int last = __reduce_max_sync(0xffffffffu, lane < C ? *cl.map_shared_rank(&pmax, lane) : INT32_MIN);
-    const long long bound = static_cast<long long>(last) - a.recent;
+    const int wm = __reduce_max_sync(0xffffffffu, pm);
+    if (lane == 0) atomicMax(&pmax, wm);
+    cl.sync();
+    const int newest = __reduce_max_sync(0xffffffffu, lane < C ? *cl.map_shared_rank(&pmax, lane) : INT32_MIN);
+    const long long bound = static_cast<long long>(newest) - a.recent;
+    if (pm > bound) {   // this thread has protected slots: the largest key
 #pragma unroll 4
-    for (int i = tid; i < n; i += EV_THREADS)
-      if (pos[lo + i] > bound) key[i] = 0xffffffffu;
+      for (int i = tid; i < n; i += EV_THREADS)
+        if (pos[lo + i] > bound) {
+          atomicSub(&hist[0][key[i] >> 24], 1u);
+          atomicAdd(&hist[0][255], 1u);
+          key[i] = 0xffffffffu;
+        }
+    }
   }
-  __syncthreads();
 
   // radix select: after each digit, `left` of the keys that share the digits so far belong to the kept;
   // when those are all of them, the digits that follow do not matter
   uint32_t prefix = 0;
   int left = keep, shift = 32, last = 0;
-  const int n32 = (n + 31) & ~31;
-  for (bool all = false; !all && shift > 0; last ^= 1) {
+  bool all = false;
+  for (; !all && shift > 0; last ^= 1) {
     shift -= 8;
     uint32_t* hp = hist[last];
-    for (int i = tid; i < n32; i += EV_THREADS) {   // whole warps
-      const uint32_t k = i < n ? key[i] : 0u;
-      const bool in = i < n && (shift == 24 || (k >> (shift + 8)) == prefix);
-      const uint32_t d = in ? (k >> shift) & 255u : 256u;
-      if (shift == 24) {   // few digits (signs and exponents): one addition per digit and warp
-        const unsigned same = __match_any_sync(0xffffffffu, d);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&hp[d], static_cast<uint32_t>(__popc(same)));
-      } else if (in) {
-        atomicAdd(&hp[d], 1u);
+    if (shift < 24)
+      for (int i = 4 * tid; i < n; i += 4 * EV_THREADS) {
+        const uint4 k4 = *reinterpret_cast<const uint4*>(key + i);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < n && (k[e] >> (shift + 8)) == prefix) atomicAdd(&hp[(k[e] >> shift) & 255u], 1u);
       }
-    }
     cl.sync();
     if (tid < 256) {
       uint32_t t = 0;
@@ -214,60 +229,84 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
     all = tot[s_digit] == static_cast<uint32_t>(left);
   }
   last ^= 1;   // the last digit's histogram
-  // keys whose first digits are above `prefix` are kept, and the first `left` of those equal to it, in slot
-  // order
-  if (warp == 0) {
-    const uint32_t e = lane < c ? cl.map_shared_rank(hist[last], lane)[prefix & 255u] : 0u;
-    s_eq0 = static_cast<int>(__reduce_add_sync(0xffffffffu, e));
-  }
-  // each warp walks a contiguous part of the slice, so that ranks follow from ballots
-  const int part = ((n + EV_WARPS - 1) / EV_WARPS + 31) & ~31;
+  // Kept are the keys whose first digits are above `prefix`, and those that equal it in slots below `tie`: all
+  // of them or, where whole keys are equal, the first `left` in slot order.
+  const int part = ((n + EV_WARPS - 1) / EV_WARPS + 127) & ~127;   // a warp's contiguous part, four slots a lane
   const int wlo = min(warp * part, n), whi = min(wlo + part, n);
-  const unsigned below = (1u << lane) - 1u;
-  int cnt = 0;
-  for (int i0 = wlo; i0 < whi; i0 += 32) {
-    const int i = i0 + lane;
-    cnt += __popc(__ballot_sync(0xffffffffu, i < whi && key[i] >> shift == prefix));
+  int tie = INT32_MAX;   // of this warp's part
+  if (!all) {
+    if (warp == 0) {
+      const uint32_t e = lane < c ? cl.map_shared_rank(hist[last], lane)[prefix & 255u] : 0u;
+      const int before = static_cast<int>(__reduce_add_sync(0xffffffffu, e));   // in the CTAs before this one
+      if (lane == 0) s_tied = left - before;
+    }
+    int cnt = 0;
+    for (int i = wlo + lane; i < whi; i += 32) cnt += key[i] == prefix;
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if (lane == 0) w_eq[warp] = cnt;
+    __syncthreads();
+    int want = s_tied;   // in this part
+    for (int w = 0; w < warp; ++w) want -= w_eq[w];
+    if (want <= 0) tie = 0;
+    for (int i0 = wlo; want > 0 && want < cnt; i0 += 32) {   // ends at the want-th
+      const bool eq = i0 + lane < whi && key[i0 + lane] == prefix;
+      const unsigned be = __ballot_sync(0xffffffffu, eq);
+      const unsigned hit = __ballot_sync(0xffffffffu, eq && __popc(be & ((1u << lane) - 1u)) == want - 1);
+      if (hit) tie = lo + i0 + __ffs(hit), cnt = 0;
+      want -= __popc(be);
+    }
   }
-  if (lane == 0) w_eq[warp] = cnt;
+  // bits 0-3: of slots i..i+3, those to be freed below `keep`; bits 4-7: those kept at or past it
+  auto events = [&](int i) {
+    const uint4 k4 = *reinterpret_cast<const uint4*>(key + i);
+    const uint32_t k[4] = {k4.x >> shift, k4.y >> shift, k4.z >> shift, k4.w >> shift};
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int slot = lo + i + e;
+      const bool kept = k[e] > prefix || (k[e] == prefix && slot < tie);
+      if (i + e < n && kept == (slot >= keep)) m |= (kept ? 16u : 1u) << e;
+    }
+    return m;
+  };
+  // twice over the part: count holes and movers (its low and high half), then (their places known) list them
+  uint32_t mine = 0;
+  for (int i = wlo + 4 * lane; i < whi; i += 128) {
+    const uint32_t m = events(i);
+    mine += __popc(m & 15u) + (__popc(m >> 4) << 16);
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) w_events[warp] = static_cast<int>(mine);
   __syncthreads();
-  int eq0 = s_eq0;
-  for (int w = 0; w < warp; ++w) eq0 += w_eq[w];
-  // twice over the part: count holes and movers, then (their places known) list them
-  int holes = 0, moves = 0;
-  for (int round = 0; round < 2; ++round) {
-    int eq = eq0, nh = holes, nm = moves;
-    for (int i0 = wlo; i0 < whi; i0 += 32) {
-      const int i = i0 + lane, slot = lo + i;
-      const bool in = i < whi;
-      const uint32_t k = in ? key[i] >> shift : 0u;
-      const unsigned be = __ballot_sync(0xffffffffu, in && k == prefix);
-      const bool kept = in && (k > prefix || (k == prefix && eq + __popc(be & below) < left));
-      const bool hole = in && !kept && slot < keep, mover = kept && slot >= keep;
-      const unsigned bh = __ballot_sync(0xffffffffu, hole), bm = __ballot_sync(0xffffffffu, mover);
-      if (round == 1) {
-        if (hole) list[nh + __popc(bh & below)] = static_cast<uint16_t>(i);
-        if (mover) list[per - 1 - nm - __popc(bm & below)] = static_cast<uint16_t>(i);
-      }
-      eq += __popc(be);
-      nh += __popc(bh);
-      nm += __popc(bm);
-    }
-    if (round == 0) {
-      if (lane == 0) {
-        w_hole[warp] = nh;
-        w_move[warp] = nm;
-      }
-      __syncthreads();
-      int th = 0, tm = 0;
-      for (int w = 0; w < EV_WARPS; ++w) {
-        if (w == warp) holes = th, moves = tm;
-        th += w_hole[w];
-        tm += w_move[w];
-      }
-      if (tid == 0) n_hole = th, n_move = tm;
-    }
+  int holes = 0, moves = 0, th = 0, tm = 0;
+  for (int w = 0; w < EV_WARPS; ++w) {
+    if (w == warp) holes = th, moves = tm;
+    th += w_events[w] & 0xffff;
+    tm += w_events[w] >> 16;
   }
+  if (tid == 0) n_hole = th, n_move = tm;
+  if (mine)
+    for (int i0 = wlo; i0 < whi; i0 += 128) {
+      const int i = i0 + 4 * lane;
+      const uint32_t m = i < whi ? events(i) : 0u;
+      if (!__any_sync(0xffffffffu, m != 0)) continue;
+      const uint32_t own = __popc(m & 15u) | (__popc(m >> 4) << 8);
+      uint32_t incl = own;   // at most 128 of either
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      int nh = holes + static_cast<int>((incl - own) & 255u), nm = moves + static_cast<int>((incl - own) >> 8);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if ((m >> e) & 1u) list[nh++] = static_cast<uint16_t>(i + e);
+        if ((m >> (4 + e)) & 1u) list[per - 1 - nm++] = static_cast<uint16_t>(i + e);
+      }
+      const uint32_t sum = __shfl_sync(0xffffffffu, incl, 31);
+      holes += static_cast<int>(sum & 255u);
+      moves += static_cast<int>(sum >> 8);
+    }
   cl.sync();   // every CTA's lists and counts
   if (warp == 0) {   // C <= 16: sums over the CTAs before each
     int th = lane < C ? *cl.map_shared_rank(&n_hole, lane) : 0;
@@ -291,18 +330,20 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
   uint4* vr = reinterpret_cast<uint4*>(a.v) + row0 * nv;
   for (int r0 = r_lo; r0 < r_hi; r0 += EV_THREADS) {
     const int nb = min(EV_THREADS, r_hi - r0);
+    float w = 0.f;
+    int q = 0, dst = 0;
     if (tid < nb) {
       const int r = r0 + tid;
       int ch = 0, cm = 0;
       while (r >= hole_base[ch + 1]) ++ch;
       while (r >= move_base[cm + 1]) ++cm;
-      const int dst = ch * per + cl.map_shared_rank(list, ch)[r - hole_base[ch]];
+      dst = ch * per + cl.map_shared_rank(list, ch)[r - hole_base[ch]];
       const int s = cm * per + cl.map_shared_rank(list, cm)[per - 1 - (r - move_base[cm])];
-      src[dst] = s;
-      acc_out[dst] = acc[s];
-      pos_out[dst] = pos[s];
       mv_dst[tid] = dst;
       mv_src[tid] = s;
+      src[dst] = s;
+      w = acc[s];   // stored behind the rows
+      q = pos[s];
     }
     __syncthreads();
     // a warp moves U rows of K and V at a time, every load before the stores
@@ -319,13 +360,17 @@ __global__ void __launch_bounds__(EV_THREADS) k_cache_evict(const __grid_constan
           if (m0 + u * EV_WARPS < nb) base[static_cast<size_t>(mv_dst[m0 + u * EV_WARPS]) * nv] = x[u];
       }
     }
+    if (tid < nb) {
+      acc_out[dst] = w;
+      pos_out[dst] = q;
+    }
     __syncthreads();
   }
   cl.sync();   // no CTA leaves while another reads its lists
 }
 
-// CTAs per cluster: as many as give the GPU two CTAs per SM, of at least 128 slots, and what shared memory
-// asks for.
+// CTAs per cluster: as many as give the GPU two CTAs per SM (figures above), of at least 128 slots, and what
+// shared memory asks for.
 int evict_cluster(int units, int S_max) {
   int C = 1;
   while (C < EV_MAX_CLUSTER && ((2 * C * units <= 296 && S_max >= 2 * C * 128) || S_max > C * 32768)) C *= 2;
