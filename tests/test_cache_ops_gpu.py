@@ -595,6 +595,91 @@ def test_evict_refuses_bad_lengths_on_the_device():
     assert e.value.code == fr.FR_ERR_DEVICE and "c001" in str(e.value)
 
 
+@pytest.mark.parametrize("spec", [
+    (4096, 2, 1, 64, 1, 40, [(7 * b) % 41 - 1 for b in range(4096)], "chain"),   # as many samples as there may be
+    (1, 1024, 1, 64, 2, 300, [271], "tree"),                  # as many heads, one KV head: sixteen row tiles
+    (2, 1024, 1024, 64, 1, 140, [139, 60], "chain"),
+    (1, 64, 1, 64, 256, 400, [140], "tree"),                  # 128 row tiles: several batches
+], ids=lambda s: "-".join(map(str, s[:6])) + "-" + s[7])
+def test_attention_and_weights_at_their_limits(spec):
+    c = Case(*spec).device()
+    c.run()
+    o = c.oracle()
+    check(c, c.o, c.lse, o)
+    acc = torch.zeros(c.B, c.Hkv, c.S, device="cuda")
+    fr.fr_attention_weights(ptr(c.dq), ptr(c.dk), ptr(c.lse), ptr(c.dlens), ptr(c.dwords), 0, ptr(acc), c.B, c.Hq, c.Hkv, c.N, c.S,
+                            c.dh, stream())
+    lse = c.lse.double().cpu().numpy()
+    want, w = R.weigh(c.q.double().numpy(), c.k.double().numpy(), lse, c.lens, c.words, None, np.zeros((c.B, c.Hkv, c.S)))
+    tl = c.dh * 2.0 ** -24 * o[3].max() + (8 + np.abs(np.where(np.isinf(o[2]), 0.0, o[2])).max()) * 2.0 ** -21
+    tol = w * (tl + c.Hq // c.Hkv * c.N * 2.0 ** -24) + 2.0 ** -23 * want + 1e-37
+    for b, n in enumerate(c.lens):
+        used = n + c.N if n >= 0 else 0
+        assert np.all(np.abs(acc[b].cpu().numpy()[:, :used] - want[b, :, :used]) <= tol[b, :, :used])
+        assert float(acc[b, :, used:].abs().sum()) == 0.0
+    assert fr.fr_ops_sync_status(stream()) == 0
+
+
+def test_bits_past_the_drafted_tokens_are_ignored():
+    """In the last word of a mask row, of the tokens in use, and in a padded sample's words."""
+    c = Case(3, 4, 2, 128, 37, 400, [300, -1, 5], "random").device()
+    use = np.zeros((3, 2), np.uint32)
+    use[:, 0], use[:, 1] = 0xF0F0F0F1, 0x15
+    res = []
+    for junk in (0, 0xFFFFFFE0):
+        c.dwords[:, :, 1] |= int(np.uint32(junk).view(np.int32))
+        c.dwords[1] = -1 if junk else 0
+        d_use = torch.from_numpy((use | np.array([0, junk], np.uint32)).view(np.int32)).cuda()
+        acc = torch.zeros(c.B, c.Hkv, c.S, device="cuda")
+        c.run()
+        fr.fr_attention_weights(ptr(c.dq), ptr(c.dk), ptr(c.lse), ptr(c.dlens), ptr(c.dwords), ptr(d_use), ptr(acc), c.B, c.Hq, c.Hkv,
+                                c.N, c.S, c.dh, stream())
+        res.append((c.o.clone(), c.lse.clone(), acc))
+    assert all(torch.equal(x, y) for x, y in zip(*res))
+    check(c, c.o, c.lse)
+
+
+@pytest.mark.parametrize("B,Hkv", [(4096, 2), (2, 1024)])
+def test_commit_and_evict_at_their_limits(B, Hkv):
+    """As many samples and heads as there may be; equal positions, so that all slots are protected."""
+    N, S, dh, keep, rng = 4, 12, 8, 5, np.random.default_rng(B)
+    lens = rng.integers(-1, S - N + 1, B).astype(np.int32)
+    npath = rng.integers(0, N + 1, B).astype(np.int32)
+    path = np.stack([np.sort(rng.permutation(N)) for _ in range(B)]).astype(np.int32)
+    for b in range(B):
+        path[b, :npath[b]] = np.sort(rng.permutation(N)[:npath[b]])
+    k = rng.standard_normal((B, Hkv, S, dh)).astype(np.float32)
+    acc, pos = rng.random((B, Hkv, S)).astype(np.float32), np.where(np.arange(B) % 2, 9, np.arange(S)[:, None]).T[:, None].repeat(Hkv, 1)
+    pos = np.ascontiguousarray(pos.astype(np.int32))
+    dk, dv, dacc, dpos = (torch.from_numpy(x).cuda() for x in (k, -k, acc, pos))
+    dl, dp, dn = (torch.from_numpy(x).cuda() for x in (lens, path, npath))
+    l2, l3 = torch.full_like(dl, 99), torch.full_like(dl, 99)
+    acc2, pos2, src = torch.full_like(dacc, MARK), torch.full_like(dpos, 7), torch.full((B, Hkv, keep), 77, dtype=torch.int32).cuda()
+    fr.fr_cache_commit(ptr(dk), ptr(dv), ptr(dacc), ptr(dpos), ptr(dl), ptr(dp), ptr(dn), ptr(l2), B, Hkv, N, S, dh, fr.FR_DTYPE_F32,
+                       stream())
+    fr.fr_cache_evict(ptr(dk), ptr(dv), ptr(dacc), ptr(dpos), ptr(l2), ptr(acc2), ptr(pos2), ptr(l3), ptr(src), B, Hkv, S, dh,
+                      fr.FR_DTYPE_F32, keep, 2, stream())
+    assert fr.fr_ops_sync_status(stream()) == 0
+    wk, wsrc = k.copy(), np.full((B, Hkv, keep), 77, np.int32)
+    wacc, wpos = acc.copy(), pos.copy()
+    racc, rpos = np.full_like(acc, MARK), np.full_like(pos, 7)
+    for b, n in enumerate(lens):
+        if n < 0:
+            continue
+        at, m = n + path[b, :npath[b]], n + npath[b]
+        for x in (wk, wacc, wpos):
+            x[b, :, n:m] = x[b][:, at]
+        for h in range(Hkv):
+            t = R.evict_one(wacc[b, h, :m], wpos[b, h, :m], keep, 2)
+            wk[b, h, :len(t)] = wk[b, h][t]
+            wsrc[b, h, :len(t)], wsrc[b, h, len(t):] = t, -1
+            racc[b, h, :len(t)], rpos[b, h, :len(t)] = wacc[b, h][t], wpos[b, h][t]
+    assert l2.tolist() == np.where(lens < 0, lens, lens + npath).tolist()
+    assert l3.tolist() == np.where(lens < 0, lens, np.minimum(lens + npath, keep)).tolist()
+    for got, want in ((dk, wk), (dv, -wk), (src, wsrc), (acc2, racc), (pos2, rpos)):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_pointers_of_the_host_are_refused():
     t = torch.zeros(4096, dtype=torch.bfloat16)
     d = torch.zeros(4096, dtype=torch.bfloat16, device="cuda")
