@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
     tmem_relinquish();
   }
   if (warp == 1) {
-    const TileRange r = tile_range(a, a.Hkv, blockIdx.x);
+    const TileRange r = tile_range<true>(a, a.Hkv, blockIdx.x);
     if ((tid & 31) == 0) range = r;
   }
   tc_fence_before();

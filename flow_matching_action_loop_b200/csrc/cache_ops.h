@@ -33,6 +33,7 @@ struct TreeArgs {
   int B, Hq, Hkv, N, W, S_max, dh;
   float scale;                 // 1/sqrt(dh)
   int rtg, groups;             // CTAs per group (row tiles of a unit), groups that share the tiles
+  int whole_extra;             // tiles that keeping a unit whole may cost a group
   int cluster;                 // attention: CTAs of a unit's cluster, 1: none
   CUtensorMap tm_q, tm_k, tm_v;   // written by the launchers
 };

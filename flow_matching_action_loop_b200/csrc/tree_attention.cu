@@ -9,6 +9,12 @@
 // so side by side over the same range of keys (with a range of its own for each, the tiles came from HBM
 // 2.6 times at 6 x 33000 slots and four row tiles).
 //
+// A cut costs a segment's end (3 us) and, by its rows, the merge.  So units are cut only where the groups would
+// otherwise have many tiles more than their share: more than a sixteenth of the rows (kept_whole); up to four tiles
+// never, above a sixteenth of the rows always (single tokens of 32 ragged samples over up to 64 tiles: 111 us cut, 129
+// with the shorter ones whole).  60 x 8/1 heads of 256, 24 tokens: 5 tiles 35.5 us cut, 24.8 whole; 80 of them: 6 tiles 45.0 and 44.1, 10 tiles
+// 55.5 and 61.3.  40 x 4/4 heads of 128, 8 tokens (8 rows): 4 tiles 20.3 and 19.8, 6 tiles 23.0 and 25.5.
+//
 // Where it costs few tiles more (tree_cluster), a unit has a cluster of up to 16 CTAs instead, its tiles in
 // equal ranges, and the cluster joins its rows over distributed shared memory: no scratch, no second kernel.
 // (First every CTA finds what each CTA counts in each row, then all threads sum four features each.  16
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
     }
     __syncwarp();
     TileRange r = {};
-    if constexpr (!CL) r = tile_range(a, a.Hkv * NB, grp);
+    if constexpr (!CL) r = tile_range<false>(a, a.Hkv * NB, grp);
     if ((tid & 31) == 0) {
       TileIter it;
       if constexpr (CL) {   // the unit's tiles in equal ranges; no further segment
@@ -713,7 +719,8 @@ constexpr int TM_THREADS = 256;
 template <int DH>
 __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant__ TreeArgs a, int split) {
   constexpr int OLD = DH + 4, FG = DH / 16;   // feature groups
-  __shared__ int sh_T, sh_cum;
+  __shared__ Line sh_line;
+  __shared__ int sh_cum;
   __shared__ float red[TM_THREADS][17];       // reference, 16 features (one split's threads after the other's)
   __shared__ float red_l[TM_THREADS], red_x[TM_THREADS];
   const int g = a.Hq / a.Hkv, R = g * a.N, RT = (R + 127) >> 7, NB = (RT + a.rtg - 1) / a.rtg;
@@ -724,8 +731,8 @@ __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant
   const int Rv = min(128, R - rt * 128), RW = min(128, R);
   const int sub = tid / (rows * FG), fg = tid / rows % FG, row = blockIdx.x * rows + tid % rows;
   if (warp == 0) {
-    const int T = tiles_before(a, U, a.B);
-    if (lane == 0) sh_T = T;
+    const Line l = measure_line(a, U, false);
+    if (lane == 0) sh_line = l;
   } else if (warp == 1) {
     const int c = tiles_before(a, U, b);
     if (lane == 0) sh_cum = c;
@@ -733,10 +740,9 @@ __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant
   const int nb = sample_tiles(a, b);
   __syncthreads();
   grid_dep_wait();
-  if (nb == 0 || blockIdx.x * rows >= Rv) return;
-  const int T = sh_T, t0 = sh_cum + (hk * NB + rt / a.rtg) * nb;
-  // group c < n holds tiles [T c / n, T (c + 1) / n), at least one
-  const int n = min(T, a.groups);
+  if (nb == 0 || blockIdx.x * rows >= Rv || kept_whole(a, sh_line, nb)) return;
+  const int T = sh_line.T, n = sh_line.n, t0 = sh_cum + (hk * NB + rt / a.rtg) * nb;
+  // group c < n holds tiles [T c / n, T (c + 1) / n) of the units that are cut, at least one
   auto holder = [&](int t) { return static_cast<int>((static_cast<long long>(t + 1) * n - 1) / T); };
   const int c0 = holder(t0), c1 = holder(t0 + nb - 1);
   if (c0 == c1) return;   // one segment: written by k_tree_attn
@@ -814,7 +820,7 @@ cudaError_t launch_tree(TreeArgs& a, cudaStream_t s) {
   }
   k_tree_attn<DH, false><<<a.groups * a.rtg, TA_THREADS, G::smem, s>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.S_max <= TREE_KEYS) return e;   // a unit of one tile is never split
+  if (e != cudaSuccess || a.S_max <= TREE_WHOLE * TREE_KEYS) return e;   // no unit is cut
   // segments per unit if every sample is as long as can be
   const int64_t units = static_cast<int64_t>(planes) * ((RT + a.rtg - 1) / a.rtg);
   const int per = static_cast<int>(a.groups / std::min<int64_t>(units, a.groups)) + 1;
@@ -875,7 +881,7 @@ int tree_cluster(const int* resident, int ctas, int64_t units, int tiles) {
 }  // namespace
 
 size_t tree_scratch_bytes(int, int Hq, int Hkv, int N, int S_max, int dh) {
-  if (S_max <= TREE_KEYS) return 0;
+  if (S_max <= TREE_WHOLE * TREE_KEYS) return 0;
   return static_cast<size_t>(2) * TA_CTAS * std::min(128, Hq / Hkv * N) * (dh + 4) * 4;
 }
 
@@ -887,6 +893,7 @@ cudaError_t launch_tree_attention(const TreeArgs& args, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int RT = (a.Hq / a.Hkv * a.N + 127) / 128, ctas = std::min(nsm, TA_CTAS);
   tree_groups(ctas, RT, a.rtg, a.groups);
+  a.whole_extra = std::min(128, a.Hq / a.Hkv * a.N) / 16;
   a.cluster = 1;
   if (dev < MAX_DEVICES)
     a.cluster = tree_cluster(g_clusters[dev][a.dh == 64 ? 0 : a.dh == 128 ? 1 : 2], ctas,

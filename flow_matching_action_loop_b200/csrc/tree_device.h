@@ -11,6 +11,7 @@ namespace fr {
 namespace tc {
 
 constexpr int TREE_KEYS = 128;   // slots per tile
+constexpr int TREE_WHOLE = 4;    // units of up to so many tiles are not cut (tree_attention.cu)
 
 __device__ __forceinline__ void report_sample(unsigned* status, uint32_t where, int sample) {
   if (!(atomicOr(status, ST_BOUNDS_BIT) & ST_BOUNDS_BIT)) {   // the first refused sample reports
@@ -26,7 +27,7 @@ __device__ __forceinline__ void report_sample(unsigned* status, uint32_t where, 
 // int.)
 struct TileRange {
   int t0, t1, cum;   // this group's tiles; first tile of sample b
-  int b, len;              // sample of t0
+  int b, len;        // sample of the unit that t0 lies in or follows
 };
 
 __device__ __forceinline__ int tiles_of(const TreeArgs& a, int len) {
@@ -82,23 +83,11 @@ __device__ __forceinline__ int tiles_before(const TreeArgs& a, int U, int b_end)
   return __reduce_add_sync(0xffffffffu, sum) * U;
 }
 
-// One warp: group c's share of the line.  The first min(T, groups) groups have at least one tile each.
-// CTA 0 reports the samples of a bad length.
-__device__ __forceinline__ TileRange tile_range(const TreeArgs& a, int U, int c) {
+// One warp: the sample that holds tile t < T, in r (b, len, cum).
+__device__ __forceinline__ void locate(const TreeArgs& a, int U, int t, TileRange& r) {
   const int lane = threadIdx.x & 31;
-  int T = 0;
-  for (int b = lane; b < a.B; b += 32) {
-    const int len = a.lens[b], n = tiles_of(a, len);
-    if (blockIdx.x == 0 && n == 0 && len >= 0) report_sample(a.status, CACHE_BAD_LEN, b);
-    T += n;
-  }
-  T = __reduce_add_sync(0xffffffffu, T) * U;
-  const int n = min(T, a.groups);
-  TileRange r = {0, 0, 0, 0, -1};
-  if (c >= n) return r;
-  r.t0 = share_begin(T, c, n);
-  r.t1 = share_begin(T, c + 1, n);
-  for (int b0 = 0; b0 < a.B; b0 += 32) {   // the sample that holds t0
+  r.cum = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int len = b0 + lane < a.B ? a.lens[b0 + lane] : -1, own = tiles_of(a, len) * U;
     int incl = own;
 #pragma unroll
@@ -106,7 +95,7 @@ __device__ __forceinline__ TileRange tile_range(const TreeArgs& a, int U, int c)
       const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, r.cum + incl > r.t0);
+    const unsigned hit = __ballot_sync(0xffffffffu, r.cum + incl > t);
     if (hit) {
       const int l = __ffs(hit) - 1;
       r.b = b0 + l;
@@ -115,6 +104,64 @@ __device__ __forceinline__ TileRange tile_range(const TreeArgs& a, int U, int c)
       break;
     }
     r.cum += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// The line's length, its units, the groups that have tiles.
+struct Line {
+  int T, units, n;
+};
+
+// One warp: the line of all samples.
+__device__ __forceinline__ Line measure_line(const TreeArgs& a, int U, bool report) {
+  int T = 0, active = 0;
+  for (int b = threadIdx.x & 31; b < a.B; b += 32) {
+    const int len = a.lens[b], n = tiles_of(a, len);
+    if (report && n == 0 && len >= 0) report_sample(a.status, CACHE_BAD_LEN, b);
+    T += n;
+    active += n > 0;
+  }
+  Line l;
+  l.T = __reduce_add_sync(0xffffffffu, T) * U;
+  l.units = __reduce_add_sync(0xffffffffu, active) * U;
+  l.n = min(l.T, a.groups);
+  return l;
+}
+
+// A unit of nb tiles is not cut if it is short (a bound moves by half of it), and the groups, with whole units of this
+// length, have at most a.whole_extra tiles more than their share of the line; see tree_attention.cu.
+__device__ __forceinline__ bool kept_whole(const TreeArgs& a, const Line& l, int nb) {
+  return nb <= TREE_WHOLE || (nb <= a.whole_extra && nb * ((l.units + l.n - 1) / l.n) <= l.T / l.n + a.whole_extra);
+}
+
+// A bound between two groups that lies in a unit that is kept whole goes to the unit's nearer end.
+__device__ __forceinline__ int move_bound(const TreeArgs& a, const Line& l, const TileRange& r, int t) {
+  const int nb = tiles_of(a, r.len);
+  if (!kept_whole(a, l, nb)) return t;
+  const int in = (t - r.cum) % nb;
+  return 2 * in > nb ? t + nb - in : t - in;
+}
+
+// One warp: group c's share of the line.  CUT: at any tile, and the first min(T, groups) groups have at least one
+// tile each.  CTA 0 reports the samples of a bad length.
+template <bool CUT>
+__device__ __forceinline__ TileRange tile_range(const TreeArgs& a, int U, int c) {
+  const Line l = measure_line(a, U, blockIdx.x == 0);
+  TileRange r = {0, 0, 0, 0, -1};
+  if (c >= l.n) return r;
+  const int t0 = share_begin(l.T, c, l.n), t1 = share_begin(l.T, c + 1, l.n);
+  locate(a, U, t0, r);
+  r.t0 = t0;
+  r.t1 = t1;
+  if constexpr (!CUT) {
+    r.t0 = move_bound(a, l, r, t0);
+    if (t1 - r.cum < U * tiles_of(a, r.len)) {   // in the same sample
+      r.t1 = move_bound(a, l, r, t1);
+    } else if (t1 < l.T) {
+      TileRange next;
+      locate(a, U, t1, next);
+      r.t1 = move_bound(a, l, next, t1);
+    }
   }
   return r;
 }

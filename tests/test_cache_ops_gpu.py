@@ -131,6 +131,10 @@ ATTEND = [
     (2, 34, 1, 64, 64, 6000, [5900, 3333], "chain"),          # 17 row tiles: two batches
     # single tokens over a cache that streams from memory: tiles land late and out of order
     (24, 32, 8, 128, 1, 4200, [4190 - 97 * i for i in range(24)], "chain"),
+    # short units whole, long ones cut, in one call
+    (70, 8, 1, 128, 16, 2600, [[100, 2584, 0, 700, -1, 1900, 511, 33][i % 8] for i in range(70)], "tree"),
+    (160, 2, 2, 64, 3, 900, [(211 * i) % 898 for i in range(160)], "random"),
+    (90, 8, 1, 256, 24, 1100, [1076 - 5 * i for i in range(90)], "tree"),
 ]
 
 
@@ -410,7 +414,7 @@ def test_tree_attention_on_two_streams_with_their_own_workspaces():
     check(b, b.o, b.lse)
 
 
-WEIGH = [s for s in ATTEND if s[5] <= 9000 and s[0] != 24]
+WEIGH = [s for s in ATTEND if s[5] <= 9000 and s[0] not in (24, 70, 90, 160)]
 
 
 @pytest.mark.parametrize("spec", WEIGH, ids=lambda s: "-".join(map(str, s[:6])) + "-" + s[7])
