@@ -12,7 +12,7 @@
 // A cut costs a segment's end (3 us) and, by its rows, the merge.  So units are cut only where the groups would
 // otherwise have many tiles more than their share: more than a sixteenth of the rows (kept_whole); up to four tiles
 // never, above a sixteenth of the rows always (single tokens of 32 ragged samples over up to 64 tiles: 111 us cut, 129
-// with the shorter ones whole).  60 x 8/1 heads of 256, 24 tokens: 5 tiles 35.5 us cut, 24.8 whole; 80 of them: 6 tiles 45.0 and 44.1, 10 tiles
+// with the shorter ones whole).  60 x 8/1 heads of 256, 24 tokens: 5 tiles 35.5 us cut, 20.2 whole; 80 of them: 6 tiles 45.0 and 44.1, 10 tiles
 // 55.5 and 61.3.  40 x 4/4 heads of 128, 8 tokens (8 rows): 4 tiles 20.3 and 19.8, 6 tiles 23.0 and 25.5.
 //
 // Where it costs few tiles more (tree_cluster), a unit has a cluster of up to 16 CTAs instead, its tiles in
@@ -730,6 +730,11 @@ __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant
   const int rows = TM_THREADS / FG / split;   // rows per CTA, side by side in a warp
   const int Rv = min(128, R - rt * 128), RW = min(128, R);
   const int sub = tid / (rows * FG), fg = tid / rows % FG, row = blockIdx.x * rows + tid % rows;
+  const int nb = sample_tiles(a, b);
+  if (nb <= TREE_WHOLE || blockIdx.x * rows >= Rv) {   // (leaves when k_tree_attn has, as what follows relies on it)
+    grid_dep_wait();
+    return;
+  }
   if (warp == 0) {
     const Line l = measure_line(a, U, false);
     if (lane == 0) sh_line = l;
@@ -737,10 +742,9 @@ __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant
     const int c = tiles_before(a, U, b);
     if (lane == 0) sh_cum = c;
   }
-  const int nb = sample_tiles(a, b);
   __syncthreads();
   grid_dep_wait();
-  if (nb == 0 || blockIdx.x * rows >= Rv || kept_whole(a, sh_line, nb)) return;
+  if (kept_whole(a, sh_line, nb)) return;
   const int T = sh_line.T, n = sh_line.n, t0 = sh_cum + (hk * NB + rt / a.rtg) * nb;
   // group c < n holds tiles [T c / n, T (c + 1) / n) of the units that are cut, at least one
   auto holder = [&](int t) { return static_cast<int>((static_cast<long long>(t + 1) * n - 1) / T); };
@@ -821,8 +825,9 @@ cudaError_t launch_tree(TreeArgs& a, cudaStream_t s) {
   k_tree_attn<DH, false><<<a.groups * a.rtg, TA_THREADS, G::smem, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.S_max <= TREE_WHOLE * TREE_KEYS) return e;   // no unit is cut
-  // segments per unit if every sample is as long as can be
   const int64_t units = static_cast<int64_t>(planes) * ((RT + a.rtg - 1) / a.rtg);
+  if (units <= a.groups && a.S_max <= a.whole_extra * TREE_KEYS) return e;   // nor here: kept_whole at any lengths
+  // segments per unit if every sample is as long as can be
   const int per = static_cast<int>(a.groups / std::min<int64_t>(units, a.groups)) + 1;
   const int split = per > 16 ? 8 : per > 8 ? 4 : per > 4 ? 2 : 1;
   const int rows = TM_THREADS / (DH / 16) / split;
