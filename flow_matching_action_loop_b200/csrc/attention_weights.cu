@@ -6,8 +6,10 @@
 // exchanged; there are no atomics.
 //
 // The 128-slot tiles of all (sample, KV head) pairs form one line, cut into equal ranges over the CTAs (one
-// per SM).  A CTA keeps up to 256 of the pair's rows in shared memory and streams its K tiles past them
-// (from the second 256 rows on out of the L2); a slot's sum is added to acc by one thread in each pass.
+// per SM).  A CTA keeps up to 256 of the pair's rows in shared memory and streams its K tiles past them, from
+// the second 256 rows on (the next pass) out of the L2.  With several passes it does so for a block of up to 128
+// tiles at a time, and its threads hold their slots' sums from pass to pass: acc receives each slot's whole sum in
+// one addition, by one thread (added pass by pass, terms far below acc would be lost one pass at a time).
 //   copy warp      query rows, K tiles by tensor map (128-byte swizzle) into a ring
 //   MMA warp       K(t) Q^T, 128 rows at a time, into one of a sum group's two score buffers in tensor memory
 //   sum warps      two groups of four take the tiles in turn, a thread a slot: 2^(s - lse) in fp32.  (With
@@ -15,8 +17,9 @@
 //                  overlap with: 1870 cycles for 128 x 128 scores against 1024 of the exponentials.)
 //
 // Single tokens of 32 samples with up to 8191 slots, 8 KV heads of 128: 59 us, 338 MB at 5.7 TB/s (memory).  Trees of
-// 63 tokens over 6 x 32767 slots, 8 query heads of 256: 49 us, 1005 TFLOP/s, the multi-function unit and the tensor
-// pipe each half busy.
+// 63 tokens over 6 x 32767 slots, 8 query heads of 256: 51 us, 965 TFLOP/s, the multi-function unit and the tensor
+// pipe each half busy; with a cold L2 55 us.  Holding the sums between the passes costs there 0.7 us; in blocks of 64
+// tiles 300 rows of 64 features over 8 x 159900 slots took 172 us instead of 156 (a pass begins with new query rows).
 #include <algorithm>
 #include <type_traits>
 
@@ -35,6 +38,13 @@ constexpr int AW_CHUNK = 128;               // rows per score buffer
 constexpr int AW_PASS = 2 * AW_CHUNK;       // rows held in shared memory
 constexpr int AW_SLOTS = 10;                // ring slots at most
 constexpr int AW_SMEM = 224 * 1024;
+constexpr int AW_HELD = 64;                 // sums that a thread holds (in local memory): its group's tiles of a block
+constexpr int AW_BLOCK = 2 * AW_HELD;       // tiles
+
+// Tile of a block of n at place i of a pass.  The groups take the places in turn, throughout.  After an odd number
+// of tiles the next pass begins with the second group (flip): the tiles change places in pairs, so that each stays
+// with its group.  Only the last one, without a partner, goes to the two groups in turn.
+__device__ __forceinline__ int tile_at(int i, int n, int flip) { return (i ^ flip) < n ? i ^ flip : i; }
 
 template <int DH>
 struct WeightGeom {
@@ -44,7 +54,8 @@ struct WeightGeom {
   static constexpr int q_bytes = AW_CHUNK * DH * 2;               // one chunk of rows
 };
 
-template <int DH>
+// MANY: more than one pass.
+template <int DH, bool MANY>
 __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_constant__ TreeArgs a) {
   using G = WeightGeom<DH>;
   extern __shared__ __align__(1024) uint8_t dsm[];
@@ -54,9 +65,10 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
   __shared__ TileRange range;
   __shared__ __align__(16) float lse_sh[AW_PASS];   // -lse in log2 units, -inf: a row that gives nothing
   __shared__ uint32_t live_sh[AW_PASS / 32];        // 0 bits: such rows of the pass, whose q may hold anything
+  __shared__ float odd_sh[TREE_KEYS];               // sums of the tile that goes from group to group
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = a.Hq / a.Hkv, R = g * a.N;
-  const int passes = (R + AW_PASS - 1) / AW_PASS;
+  const int passes = MANY ? (R + AW_PASS - 1) / AW_PASS : 1;
   // the query rows of a pass take as many chunks as the largest pass has; the ring has the rest
   const int q_chunks = R > AW_CHUNK ? 2 : 1;
   const int NS = min(AW_SLOTS, (AW_SMEM - q_chunks * G::q_bytes) / G::piece);
@@ -97,13 +109,15 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
   it.start(a, rg, a.Hkv);
   bool ok = true;
   auto pass_rows = [&](int p) { return min(AW_PASS, R - p * AW_PASS); };
+  constexpr int block = MANY ? AW_BLOCK : INT_MAX;
 
   if (warp == AW_SUM / 32) {
     // ---------------- copies
     if ((tid & 31) == 0) {
-      int slot = 0, use = 0, q_use = 0, issued = 0;
-      while (ok && it.next(a, 1, 1, 0)) {
-        const int plane = it.b * a.Hkv + it.hk;
+      int slot = 0, use = 0, q_use = 0, issued = 0, turn = 0;
+      bool more = it.next(a, 1, 1, 0);
+      for (int b0 = it.tile0; ok && more;) {
+        const int plane = it.b * a.Hkv + it.hk, n = min(block, it.tile1 - b0);
         for (int p = 0; ok && p < passes; ++p) {
           if (q_use > 0 && !mbar_wait(&q_empty, (q_use - 1) & 1, WAIT_LIMIT_NS)) {
             ok = false;
@@ -114,7 +128,8 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
           mbar_arrive_expect_tx(&q_full, nc * G::q_bytes);
           for (int c = 0; c < nc; ++c)
             tma_load_4d(dsm + c * G::q_bytes, &a.tm_q, 0, p * AW_PASS + c * AW_CHUNK, 0, plane, &q_full);
-          for (int tile = it.tile0; ok && tile < it.tile1; ++tile)
+          for (int at = 0; ok && at < n; ++at) {
+            const int tile = b0 + tile_at(at, n, MANY ? turn : 0);
             for (int i = 0; i < G::pieces; ++i) {
               if ((use > 0 && !mbar_wait(&empty[slot], (use - 1) & 1, WAIT_LIMIT_NS)) || *abort_v) {
                 ok = false;
@@ -125,6 +140,13 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
               ++issued;
               if (++slot == NS) slot = 0, ++use;
             }
+          }
+          turn ^= n & 1;
+        }
+        b0 += n;
+        if (b0 >= it.tile1) {
+          more = it.next(a, 1, 1, 0);
+          b0 = it.tile0;
         }
       }
       if (!ok) {
@@ -145,8 +167,13 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
     auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };   // known to be uniform
     const uint64_t dq = smem_desc_sw128(smem_u32(dsm), 16, 1024), dk = smem_desc_sw128(smem_u32(ring), 16, 1024);
     int slot = 0, use = 0, q_use = 0, grp = 0, items[2] = {0, 0};   // group of the next tile, items of each group
-    while (ok && same(it.next(a, 1, 1, 0))) {
-      const int tiles = same(it.tile1 - it.tile0);
+    for (int to_go = 0; ok;) {   // tiles of the segment
+      if (to_go == 0) {
+        if (!same(it.next(a, 1, 1, 0))) break;
+        to_go = same(it.tile1 - it.tile0);
+      }
+      const int tiles = min(block, to_go);
+      to_go -= tiles;
       for (int p = 0; ok && p < passes; ++p) {
         ok = ok_wait(&q_full, q_use);
         ++q_use;
@@ -200,8 +227,10 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in log2 units
     const uint64_t sl22 = pack_f32x2(sl2, sl2);
     int item = 0, turn = 0;                            // of this group; group of the next tile
-    while (it.next(a, 1, 1, 0)) {
-      const int len = it.len, keys = len + a.N;
+    float held[MANY ? AW_HELD : 1];                    // sums of this thread's slots over the passes so far
+    bool more = it.next(a, 1, 1, 0);
+    for (int b0 = it.tile0; more;) {
+      const int len = it.len, keys = len + a.N, n = min(block, it.tile1 - b0);
       float* acc = a.acc + (static_cast<size_t>(it.b) * a.Hkv + it.hk) * a.S_max;
       const float* lse = a.lse + (static_cast<size_t>(it.b) * a.Hq + static_cast<size_t>(it.hk) * g) * a.N;
       for (int p = 0; p < passes; ++p) {
@@ -210,8 +239,8 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
         {
           float x = -INFINITY;
           if (tid < rows) {
-            const int n = (r0 + tid) % a.N;
-            const bool counts = !a.use || ((a.use[static_cast<size_t>(it.b) * a.W + (n >> 5)] >> (n & 31)) & 1u);
+            const int tok = (r0 + tid) % a.N;
+            const bool counts = !a.use || ((a.use[static_cast<size_t>(it.b) * a.W + (tok >> 5)] >> (tok & 31)) & 1u);
             const float v = lse[r0 + tid];
             if (counts && v != -INFINITY) x = -v * 1.4426950408889634f;
           }
@@ -220,15 +249,21 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
           if (lane == 0) live_sh[warp] = live;
         }
         asm volatile("bar.sync 5, 256;" ::: "memory");
-        // a committed slot adds to its sum, a drafted one begins with the first rows; fetched a tile ahead
-        auto sum_before = [&](int tile) { return acc[min(tile * TREE_KEYS + key, keys - 1)]; };
-        const int first = it.tile0 + (turn ^ grp);   // this group's tiles: every other one
-        turn ^= (it.tile1 - it.tile0) & 1;
+        // a committed slot adds to its sum, a drafted one begins with these rows; fetched a tile ahead
+        const bool last = p == passes - 1;
+        const int flip = MANY ? turn : 0;
+        auto sum_before = [&](int at) {
+          return last ? acc[min((b0 + tile_at(at, n, flip)) * TREE_KEYS + key, keys - 1)] : 0.f;
+        };
+        const int first = turn ^ grp;   // this group's places: every other one
+        turn ^= n & 1;
         float before = sum_before(first);
-        for (int tile = first; tile < it.tile1; tile += 2) {
-          const int slot = tile * TREE_KEYS + key;
+        for (int at = first; at < n; at += 2) {
+          const int in_block = tile_at(at, n, flip), tile = b0 + in_block, slot = tile * TREE_KEYS + key;
           const bool boundary = (tile + 1) * TREE_KEYS > len;
-          const float next = sum_before(tile + 2);
+          const float next = sum_before(at + 2);
+          float* part = !MANY ? nullptr : (n & 1) && in_block == n - 1 ? &odd_sh[key] : &held[in_block >> 1];
+          const float so_far = MANY && p > 0 ? *part : 0.f;
           uint64_t w2[2] = {0, 0};
           for (int c = 0; c < nc; ++c, ++item) {
             const int buf = 2 * grp + (item & 1);
@@ -240,9 +275,9 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
             if (boundary) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int n = (r0 + c * AW_CHUNK + 32 * i + lane) % a.N;
-                const uint32_t* words = a.mask ? a.mask + (static_cast<size_t>(it.b) * a.N + n) * a.W : nullptr;
-                vis[i] = seen_slots(words, n, a.N, a.W, tile * TREE_KEYS + 32 * pw - len);
+                const int tok = (r0 + c * AW_CHUNK + 32 * i + lane) % a.N;
+                const uint32_t* words = a.mask ? a.mask + (static_cast<size_t>(it.b) * a.N + tok) * a.W : nullptr;
+                vis[i] = seen_slots(words, tok, a.N, a.W, tile * TREE_KEYS + 32 * pw - len);
               }
               auto stage = [&](int st, uint32_t m) {   // the four words side by side: a shuffle waits long
                 uint32_t y[4];
@@ -305,9 +340,16 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
             if (lane == 0) mbar_arrive(&bar_e[buf]);
           }
           const float2 wp = unpack_f32x2(add_f32x2(w2[0], w2[1]));
-          if (slot < keys && ok) acc[slot] = (slot < len || p > 0 ? before : 0.f) + (wp.x + wp.y);
+          const float w = so_far + (wp.x + wp.y);
+          if (MANY && !last) *part = w;
+          if (last && slot < keys && ok) acc[slot] = (slot < len ? before : 0.f) + w;
           before = next;
         }
+      }
+      b0 += n;
+      if (b0 >= it.tile1) {
+        more = it.next(a, 1, 1, 0);
+        b0 = it.tile0;
       }
     }
     if (!ok) {
@@ -330,18 +372,19 @@ cudaError_t launch_weights(TreeArgs& a, cudaStream_t s) {
   if (!encode_rows_map(&a.tm_q, a.q, DH, R, R, planes, AW_CHUNK, DH / 64) ||
       !encode_rows_map(&a.tm_k, a.k, DH, a.S_max, a.S_max, planes, TREE_KEYS, G::blocks))
     return cudaErrorInvalidValue;
-  k_attn_weights<DH><<<a.groups, AW_THREADS, AW_SMEM, s>>>(a);
+  (R > AW_PASS ? k_attn_weights<DH, true> : k_attn_weights<DH, false>)<<<a.groups, AW_THREADS, AW_SMEM, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t weights_init() {
-  cudaError_t e;
-  const auto at = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  if ((e = cudaFuncSetAttribute(k_attn_weights<64>, at, AW_SMEM)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(k_attn_weights<128>, at, AW_SMEM)) != cudaSuccess) return e;
-  return cudaFuncSetAttribute(k_attn_weights<256>, at, AW_SMEM);
+  for (auto f : {k_attn_weights<64, false>, k_attn_weights<128, false>, k_attn_weights<256, false>,
+                 k_attn_weights<64, true>, k_attn_weights<128, true>, k_attn_weights<256, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, AW_SMEM);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_attention_weights(const TreeArgs& args, cudaStream_t s) {

@@ -789,3 +789,53 @@ def test_a_run_together_on_a_handles_cache():
         acc, acc2, pos, pos2, lens, lens2 = acc2, acc, pos2, pos, lens2, lens
     assert fr.fr_ops_sync_status(stream()) == 0
     backbone.close()
+
+
+def weigh_on_the_gpu(c, lse, acc):
+    """R.weigh on the GPU in 64 bits, all tokens in use: for caches too long for the numpy loops."""
+    out, weight, g = acc.double().clone(), torch.zeros_like(acc, dtype=torch.float64), c.Hq // c.Hkv
+    for b, n in enumerate(c.lens):
+        if n < 0:
+            continue
+        hidden = torch.from_numpy(~R.sees(None if c.words is None else c.words[b], c.N)).cuda()
+        for h in range(c.Hq):
+            x = c.dq[b, h].double() @ c.dk[b, h // g, :n + c.N].double().T / c.dh ** 0.5 - lse[b, h].double()[:, None]
+            x[:, n:][hidden] = float("-inf")
+            weight[b, h // g, :n + c.N] += torch.where((lse[b, h] == float("-inf"))[:, None], 0.0, torch.exp(x)).sum(0)
+        out[b, :, :n] += weight[b, :, :n]
+        out[b, :, n:n + c.N] = weight[b, :, n:n + c.N]
+    return out, weight
+
+
+# rows of a KV head past 256 are summed in several passes: two with one, two and many tiles per CTA, three, eight,
+# 64; blocks of tiles within a CTA's share (the last)
+MANY_ROWS = [(1, 8, 1, 256, 63, 300, [200], "tree"), (6, 8, 1, 256, 63, 9000, [8900, 7000, 8555, 130, -1, 0], "tree"),
+             (2, 6, 2, 128, 130, 2300, [2100, 1999], "chain"), (7, 3, 1, 64, 256, 40000, [39000 + 31 * b for b in range(7)], "tree"),
+             (3, 8, 1, 128, 256, 6000, [5700, 3333, 40], "tree"), (1, 64, 1, 64, 256, 400, [140], "tree"),
+             (8, 6, 2, 64, 100, 160000, [159900 - 7 * b for b in range(8)], "tree")]
+
+
+@pytest.mark.parametrize("spec", MANY_ROWS, ids=lambda s: "-".join(map(str, s[:6])) + "-" + s[7])
+def test_weights_of_many_rows_are_added_to_large_sums_at_once(spec):
+    """A slot's sum over all rows is one float32 value, added with one rounding: half a step of the result, 2^-24,
+    beside the error of the sum itself."""
+    c = Case(*spec)
+    rows = c.Hq // c.Hkv * c.N
+    assert rows > 256
+    c.device().run()
+    acc = (500 + 1500 * torch.rand(c.B, c.Hkv, c.S, generator=torch.Generator().manual_seed(1))).cuda()
+    want, w = weigh_on_the_gpu(c, c.lse, acc)
+    got = [acc.clone() for _ in range(2)]
+    for x in got:
+        fr.fr_attention_weights(ptr(c.dq), ptr(c.dk), ptr(c.lse), ptr(c.dlens), ptr(c.dwords), 0, ptr(x), c.B, c.Hq, c.Hkv, c.N, c.S,
+                                c.dh, stream())
+    assert torch.equal(*got) and fr.fr_ops_sync_status(stream()) == 0
+    # |q| |k| bounds sum|q_d k_d|; |lse| is at most the largest score and the log of the slots
+    live = [b for b, n in enumerate(c.lens) if n >= 0]
+    size = max(float((c.dq[b].float().norm(dim=-1).max() * c.dk[b, :, :c.lens[b] + c.N].float().norm(dim=-1).max())) for b in live) / c.dh ** 0.5
+    tl = c.dh * 2.0 ** -24 * size + (8 + size + np.log(c.S)) * 2.0 ** -21
+    for b, n in enumerate(c.lens):
+        m = n + c.N if n >= 0 else 0
+        d = (got[0][b].double() - want[b]).abs()
+        assert torch.all(d[:, :m] <= w[b, :, :m] * (tl + rows * 2.0 ** -24) + 2.0 ** -24 * want[b, :, :m] + 1e-37), float(d[:, :m].max())
+        assert torch.equal(got[0][b, :, m:], acc[b, :, m:])
