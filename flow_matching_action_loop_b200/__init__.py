@@ -23,7 +23,7 @@ from ._abi import (  # noqa: F401
     fr_device_checks, fr_debug_limit_extent,
     FR_ATTENTION_NOALLOC_SCRATCH_BYTES, FR_CACHE_MAX_SLOTS, FR_CAPSULE_MAGIC, FR_EVICT_MAX_SLOTS, FR_TREE_MAX_NODES,
     fr_attention_tree, fr_attention_tree_scratch_bytes, fr_attention_weights, fr_cache_commit, fr_cache_evict,
-    fr_tree_mask, FR_PREFIX_K_ROTATED, FrCapsule, FrConfig, FrError,
+    fr_tree_mask, fr_ops_set_wait_limit, FR_PREFIX_K_ROTATED, FrCapsule, FrConfig, FrError,
     fr_attention, fr_attention_noalloc, fr_attention_scratch_bytes, fr_ops_sync_status, fr_calibrate, fr_capsule_bytes,
     fr_capsule_restore, fr_capsule_save, fr_create, fr_denoise, fr_destroy, fr_get_buffer, fr_get_rope_tables,
     fr_get_scales, fr_graph_count, fr_last_error, fr_launches_per_call, fr_load_weights, fr_path_name,

@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
       for (int b0 = it.tile0; ok && more;) {
         const int plane = it.b * a.Hkv + it.hk, n = min(block, it.tile1 - b0);
         for (int p = 0; ok && p < passes; ++p) {
-          if (q_use > 0 && !mbar_wait(&q_empty, (q_use - 1) & 1, WAIT_LIMIT_NS)) {
+          if (q_use > 0 && !tree_wait(&q_empty, (q_use - 1) & 1, a.wait_ns)) {
             ok = false;
             break;
           }
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
           for (int at = 0; ok && at < n; ++at) {
             const int tile = b0 + tile_at(at, n, MANY ? turn : 0);
             for (int i = 0; i < G::pieces; ++i) {
-              if ((use > 0 && !mbar_wait(&empty[slot], (use - 1) & 1, WAIT_LIMIT_NS)) || *abort_v) {
+              if ((use > 0 && !tree_wait(&empty[slot], (use - 1) & 1, a.wait_ns)) || *abort_v) {
                 ok = false;
                 break;
               }
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
     const bool leader = elect_one();
     auto ok_wait = [&](uint64_t* bar, int phase) {
       if (__all_sync(0xffffffffu, mbar_test(bar, phase & 1))) return true;
-      return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, WAIT_LIMIT_NS) && !*abort_v) != 0;
+      return __all_sync(0xffffffffu, tree_wait(bar, phase & 1, a.wait_ns) && !*abort_v) != 0;
     };
     auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };   // known to be uniform
     const uint64_t dq = smem_desc_sw128(smem_u32(dsm), 16, 1024), dk = smem_desc_sw128(smem_u32(ring), 16, 1024);
@@ -220,8 +220,9 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
     mma_commit_warp(leader, &fin_bar);
     if (!mbar_wait(&fin_bar, 0, WAIT_LIMIT_NS) && leader) report_timeout(a.status, 0x722);
   } else {
-    // ---------------- sums.  A warp whose wait gave up goes on without waiting (the named barrier needs
-    // every warp) and stores nothing.
+    // ---------------- sums.  A warp whose wait gave up goes on without waiting (the named barrier needs every
+    // warp).  Its arrivals come too early from then on: it sets the abort word before them, and no sum is stored
+    // that was read after that.
     const int key = tid & 127, grp = tid >> 7, pw = warp & 3, lane = tid & 31;   // slot of the tile, group
     const uint32_t lanes = static_cast<uint32_t>(pw * 32) << 16;
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in log2 units
@@ -295,8 +296,10 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) vis[i] &= live_sh[4 * c + i];
-            if (!__all_sync(0xffffffffu, mbar_test(&bar_s[buf], (item >> 1) & 1)) && ok)
-              ok = __all_sync(0xffffffffu, mbar_wait(&bar_s[buf], (item >> 1) & 1, WAIT_LIMIT_NS) && !*abort_v);
+            if (!__all_sync(0xffffffffu, mbar_test(&bar_s[buf], (item >> 1) & 1)) && ok) {
+              ok = __all_sync(0xffffffffu, tree_wait(&bar_s[buf], (item >> 1) & 1, a.wait_ns) && !*abort_v);
+              if (!ok) *abort_v = 1;
+            }
             tc_fence_after();
             const uint32_t ts = tS + buf * AW_CHUNK + lanes;
             // all: every column counts, for every slot
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
           const float2 wp = unpack_f32x2(add_f32x2(w2[0], w2[1]));
           const float w = so_far + (wp.x + wp.y);
           if (MANY && !last) *part = w;
-          if (last && slot < keys && ok) acc[slot] = (slot < len ? before : 0.f) + w;
+          if (last && slot < keys && !*abort_v) acc[slot] = (slot < len ? before : 0.f) + w;
           before = next;
         }
       }

@@ -1,11 +1,13 @@
 // Entry points of the cache ops: tree attention, accumulated attention weights, commit of accepted
 // drafted tokens, eviction.  Argument checks here, kernels in tree_attention.cu and cache_moves.cu.
+#include <atomic>
 #include <cmath>
 
 #include <cuda.h>
 
 #include "cache_ops.h"
 #include "internal.h"
+#include "tc_kernels.h"
 
 namespace fr {
 namespace {
@@ -48,6 +50,8 @@ int check_pointers(const char* op, const void* const* ptrs, int n) {
   }
   return FR_OK;
 }
+
+std::atomic<uint64_t> g_wait_ns{tc::WAIT_LIMIT_NS};
 
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
@@ -96,6 +100,15 @@ int check_move_sizes(const char* op, int B, int Hkv, int S_max, int dh, int dtyp
 using namespace fr;
 
 extern "C" {
+
+int fr_ops_set_wait_limit(uint64_t limit_ns) {
+  if (limit_ns > 10000000000ull) {
+    set_error("fr_ops_set_wait_limit: limit above 10 s");
+    return FR_ERR_ARG;
+  }
+  g_wait_ns = limit_ns ? limit_ns : tc::WAIT_LIMIT_NS;
+  return FR_OK;
+}
 
 int fr_tree_mask(const int32_t* parents, int n, uint32_t* mask) {
   if (!parents || !mask) {
@@ -155,6 +168,7 @@ int fr_attention_tree(const void* q, const void* k, const void* v, const int32_t
   a.scratch = static_cast<float*>(scratch);
   a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.N = N, a.W = (N + 31) / 32, a.S_max = S_max, a.dh = dh;
   a.scale = 1.0f / std::sqrt(static_cast<float>(dh));
+  a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   FR_CUDA(tc::launch_tree_attention(a, reinterpret_cast<cudaStream_t>(stream)));
   return FR_OK;
 }
@@ -183,6 +197,7 @@ int fr_attention_weights(const void* q, const void* k, const float* lse, const i
   a.acc = acc;
   a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.N = N, a.W = (N + 31) / 32, a.S_max = S_max, a.dh = dh;
   a.scale = 1.0f / std::sqrt(static_cast<float>(dh));
+  a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   FR_CUDA(tc::launch_attention_weights(a, reinterpret_cast<cudaStream_t>(stream)));
   return FR_OK;
 }

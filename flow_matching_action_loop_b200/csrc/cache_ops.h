@@ -32,6 +32,7 @@ struct TreeArgs {
   unsigned* status;
   int B, Hq, Hkv, N, W, S_max, dh;
   float scale;                 // 1/sqrt(dh)
+  uint64_t wait_ns;            // bound of a wait (fr_ops_set_wait_limit)
   int rtg, groups;             // CTAs per group (row tiles of a unit), groups that share the tiles
   int whole_extra;             // tiles that keeping a unit whole may cost a group
   int cluster;                 // attention: CTAs of a unit's cluster, 1: none

@@ -106,8 +106,10 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // 16 features of a row joined over segments: O and the sum brought to the largest reference.
 struct MergedRow {
   float m = -INFINITY, l = 0.f, x = 0.f, o[16] = {};
+  bool lost = false;   // a segment whose CTA gave up: its reference is NaN (that of scores never is)
   __device__ __forceinline__ void add(float m2, float l2, float x2, const float* v) {
     const float mn = fmaxf(m, m2);
+    lost |= m2 != m2;
     x += x2;   // NaN where a drafted value row was not finite
     if (mn == -INFINITY) {   // no score above -inf: the sums are 0, or NaN with the scores
       l += l2;
@@ -156,19 +158,19 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
   volatile int* abort_v = &abort_flag;
   bool ok = true;
 
-  // the copies' state: next ring position, segments begun
-  int pos = 0, seg = -1;
+  // the copies' state: next ring position, segments whose queries have been fetched
+  int pos = 0, segs = 0;
   auto load_q = [&](const TileIter& it) {
-    ++seg;
-    const int qb = seg % G::QB, use = seg / G::QB;
-    if (use > 0 && !mbar_wait(&q_empty[qb], (use - 1) & 1, WAIT_LIMIT_NS)) return false;
+    const int qb = segs % G::QB, use = segs / G::QB;
+    if (use > 0 && !tree_wait(&q_empty[qb], (use - 1) & 1, a.wait_ns)) return false;
+    ++segs;
     mbar_arrive_expect_tx(&q_full[qb], G::q_bytes);
     tma_load_4d(dsm + qb * G::q_bytes, &a.tm_q, 0, it.rt * 128, 0, it.b * a.Hkv + it.hk, &q_full[qb]);
     return true;
   };
   auto load_piece = [&](const CUtensorMap* tm, int key, int block, int plane) {
     const int s = pos % G::NS, use = pos / G::NS;
-    if ((use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, WAIT_LIMIT_NS)) || *abort_v) return false;
+    if ((use > 0 && !tree_wait(&empty[s], (use - 1) & 1, a.wait_ns)) || *abort_v) return false;
     mbar_arrive_expect_tx(&full[s], G::piece);
     tma_load_4d(ring + s * G::piece, tm, 0, key, block, plane, &full[s]);
     ++pos;
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         if (i >= 0 ? i % 2 != 0 || i / 2 + G::LA < nk : i + G::LA < nk)   // not a place left out
           mbar_wait(&full[p % G::NS], (p / G::NS) & 1, WAIT_LIMIT_NS);
       }
-      for (int s = max(0, seg - G::QB + 1); s <= seg; ++s)
+      for (int s = max(0, segs - G::QB); s < segs; ++s)
         mbar_wait(&q_full[s % G::QB], (s / G::QB) & 1, WAIT_LIMIT_NS);
     }
   } else if (warp == TA_SOFTMAX / 32 + 1) {
@@ -313,6 +315,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
       const uint64_t dq = smem_desc_sw128(smem_u32(dsm), 16, 1024), dk = smem_desc_sw128(smem_u32(ring), 16, 1024),
                      dv = smem_desc_sw128(smem_u32(ring), G::v_keys * 128, 1024);   // + byte offset / 16
       uint64_t idle = 0;
+      const uint64_t limit = a.wait_ns - 1;
       for (;;) {
         const int pk = G::pieces * (ts < G::LA ? ts : 2 * ts - G::LA), pv = G::pieces * (2 * tv + G::LA + 1);
         // every test is on its way before the first answer is used: one after the other they took 700 cycles
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         } else {
           const uint64_t now = globaltimer();
           if (idle == 0) idle = now;
-          if (__any_sync(0xffffffffu, now - idle > WAIT_LIMIT_NS || *abort_v)) {
+          if (__any_sync(0xffffffffu, now - idle >= limit || *abort_v)) {
             ok = false;
             break;
           }
@@ -393,14 +396,17 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
   }
   } else {
     regs_grow<TA_REGS_SOFTMAX>();
-    // ---------------- softmax.  A warp whose wait gave up goes on without waiting (the named barriers
-    // need every warp) and stores nothing.
+    // ---------------- softmax.  A warp whose wait gave up goes on without waiting (the named barriers need every
+    // warp).  Its arrivals come too early from then on, so that no row of the CTA can be trusted: it sets the abort
+    // word before them, and nothing is stored, and no partial row counts, that was read after that.
     const int row = tid & 127, hh = tid >> 7, pw = warp & 3;   // row of the tile, group, lane quadrant
     const uint32_t lanes = static_cast<uint32_t>(pw * 32) << 16;
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in log2 units
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!__all_sync(0xffffffffu, mbar_test(bar, parity)) && ok)
-        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, WAIT_LIMIT_NS) && !*abort_v);
+      if (!__all_sync(0xffffffffu, mbar_test(bar, parity)) && ok) {
+        ok = __all_sync(0xffffffffu, tree_wait(bar, parity, a.wait_ns) && !*abort_v);
+        if (!ok) *abort_v = 1;
+      }
       tc_fence_after();
     };
     int t = 0, nbound = 0;
@@ -572,7 +578,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         const float lt = fabsf(l0) * exp2f(r0 - at) + fabsf(l1) * exp2f(r1 - at);
         const float bad_v = signbit(l0) || signbit(l1) ? NAN : 0.f;
         const bool whole = !CL && it.tile1 - it.tile0 == it.nb;
-        const bool mine = row < Rv && ok;
+        const bool mine = row < Rv;
         const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) + bad_v : 1.f;
         __nv_bfloat16* orow = a.o + (static_cast<size_t>(it.b) * a.N + tok) * a.Hq * DH + static_cast<size_t>(hq) * DH;
         // a partial segment's rows: [dh / 4][rows][4] floats, then (reference, sum, spoilt) [rows][4], so
@@ -586,7 +592,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
           uint32_t ov[32];
           tmem_ld32_nowait(tO + lanes + c0, ov);
           tmem_wait_ld();
-          if (!mine || !work) continue;
+          if (!mine || (!CL && whole && *abort_v)) continue;
           if (whole) {
 #pragma unroll
             for (int e = 0; e < 32; e += 16) {
@@ -603,16 +609,17 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
                   make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
           }
         }
+        tc_fence_before();
+        pair_barrier(pw);   // both groups have read O and the sums before either goes on
         if (mine && hh == 0) {
+          const bool lost = *abort_v != 0;   // then what either group has read may be wrong, or was left out
           if (!whole) {
             *reinterpret_cast<float4*>(part + static_cast<size_t>(DH / 4) * RW * 4) =
-                make_float4(ref, CL ? copysignf(lt, bad_v != bad_v ? -1.f : 1.f) : lt, bad_v, 0.f);
-          } else if (a.lse) {
+                make_float4(!CL && lost ? NAN : ref, CL ? copysignf(lt, bad_v != bad_v ? -1.f : 1.f) : lt, bad_v, 0.f);
+          } else if (a.lse && !lost) {
             a.lse[(static_cast<size_t>(it.b) * a.Hq + hq) * a.N + tok] = row_lse(ref, lt);
           }
         }
-        tc_fence_before();
-        pair_barrier(pw);   // both groups have read O and the sums before either goes on
       }
     }
     if (!ok) {
@@ -622,6 +629,9 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
   }
   __syncthreads();
   if constexpr (CL) {
+    // A CTA that gave up says so in its rows' references, now that no copy of its own can land on them any more.
+    if (*abort_v && tid < 128) reinterpret_cast<float*>(dsm)[(DH / 4 * 128 + tid) * 4] = NAN;
+    __syncwarp();
     cluster_arrive();
     // What follows is every warp's.  (Behind the block's barrier: a warp that took its registers back before the
     // softmax warps had theirs would leave them waiting for good.)
@@ -649,6 +659,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
     };
     // every CTA: what each of them counts in each row, 2^(reference - largest) / sum
     float* weight = reinterpret_cast<float*>(dsm) + (DH / 4 + 1) * 128 * 4;   // [CTA][row]
+    bool lost = false;   // a CTA gave up
     if (tid < Rv) {
       float2 st[TA_CLUSTER];   // reference, sum
 #pragma unroll
@@ -661,6 +672,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
 #pragma unroll
       for (int k = 0; k < TA_CLUSTER; ++k) {
         m = fmaxf(m, st[k].x);
+        lost |= st[k].x != st[k].x;
         spoilt |= signbit(st[k].y);
       }
       const float at = m == -INFINITY ? 0.f : m;
@@ -674,14 +686,14 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
 #pragma unroll
       for (int k = 0; k < TA_CLUSTER; ++k)
         if (k < n) weight[k * 128 + tid] = st[k].x * inv;
-      if (a.lse && me == 0 && n > 0) {
+      if (a.lse && me == 0 && n > 0 && !lost) {
         const int rr = u.rt * 128 + tid, hq = u.hk * g + rr / a.N;
         a.lse[(static_cast<size_t>(u.b) * a.Hq + hq) * a.N + rr % a.N] = row_lse(m, l);
       }
     }
-    __syncthreads();
+    lost = __syncthreads_or(lost) != 0;
     // four features of a row a thread, the warps' items in turn over the CTAs
-    const int items = n > 0 ? Rv * (DH / 4) : 0;
+    const int items = n > 0 && !lost ? Rv * (DH / 4) : 0;
     for (int i = ((tid >> 5) * C + me) * 32 + (tid & 31); i < items; i += C * TA_THREADS) {
       const int f4 = i / Rv, row = i - f4 * Rv, rr = u.rt * 128 + row;
       float o[4] = {};
@@ -773,7 +785,7 @@ __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant
     }
   }
   if (split > 1) {
-    red[tid][0] = m.m;
+    red[tid][0] = m.lost ? NAN : m.m;
 #pragma unroll
     for (int e = 0; e < 16; ++e) red[tid][e + 1] = m.o[e];
     red_l[tid] = m.l;
@@ -782,7 +794,7 @@ __global__ void __launch_bounds__(TM_THREADS) k_tree_merge(const __grid_constant
     if (sub == 0)
       for (int w = tid + rows * FG; w < TM_THREADS; w += rows * FG) m.add(red[w][0], red_l[w], red_x[w], &red[w][1]);
   }
-  if (row >= Rv || sub != 0) return;
+  if (row >= Rv || sub != 0 || m.lost) return;
   m.store(a, b, hk, rt * 128 + row, fg, DH);
 }
 

@@ -166,6 +166,16 @@ __device__ __forceinline__ TileRange tile_range(const TreeArgs& a, int U, int c)
   return r;
 }
 
+// A wait of at most limit_ns; at 1 ns the one test that it begins with (mbar_wait's own first test may suspend the
+// thread for longer).
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (limit_ns == 1) return sm100::mbar_test(bar, parity);
+  const uint64_t t0 = sm100::globaltimer();
+  while (!sm100::mbar_try_wait(bar, parity))
+    if (sm100::globaltimer() - t0 > limit_ns) return false;
+  return true;
+}
+
 // Two float32 operations per instruction (sm_100), each rounded to nearest.
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
   uint64_t r;

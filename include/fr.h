@@ -518,6 +518,13 @@ int fr_attention_noalloc(const void* q, const void* k, const void* v, void* o, i
  *     FR_ERR_UNSUPPORTED (limits), FR_ERR_CUDA.
  */
 
+/* fr_ops_set_wait_limit -- bound, in ns, of each wait inside the kernels of fr_attention_tree and
+ * fr_attention_weights, for the calls of this process from then on (0 restores the default, 2 s; at 1 ns a wait
+ * gives up that is not over when it begins).  A wait that gives up latches FR_ERR_TIMEOUT in the ops' status word
+ * (fr_ops_sync_status); what the call has written by then is right, the rest of o, lse and acc stays as it was.
+ * Errors: FR_ERR_ARG (limit above 10 s). */
+int fr_ops_set_wait_limit(uint64_t limit_ns);
+
 /* Drafted tokens per sample, and tokens of a sample, at most. */
 #define FR_TREE_MAX_NODES 256
 #define FR_CACHE_MAX_SLOTS (1 << 24)

@@ -839,3 +839,60 @@ def test_weights_of_many_rows_are_added_to_large_sums_at_once(spec):
         d = (got[0][b].double() - want[b]).abs()
         assert torch.all(d[:, :m] <= w[b, :, :m] * (tl + rows * 2.0 ** -24) + 2.0 ** -24 * want[b, :, :m] + 1e-37), float(d[:, :m].max())
         assert torch.equal(got[0][b, :, m:], acc[b, :, m:])
+
+
+# a cluster per unit (one and several samples), units whole, cut units that the merge joins, several row tiles, batches of them
+GIVE_UP = [(1, 8, 1, 256, 1, 866, [816], "chain"), (2, 16, 16, 64, 128, 4300, [4095, 3900], "chain"), (4, 16, 2, 128, 24, 2148, [2048, 1500, -1, 9], "tree"),
+           (40, 8, 8, 64, 1, 200, [150 + b for b in range(40)], "chain"), (24, 32, 8, 128, 1, 4200, [4190 - 97 * b for b in range(24)], "chain"),
+           (6, 8, 1, 256, 63, 9000, [8900 - 500 * b for b in range(6)], "tree"), (2, 34, 1, 64, 64, 6000, [5900, 3333], "chain")]
+
+
+@pytest.mark.parametrize("spec", GIVE_UP, ids=lambda s: "-".join(map(str, s[:6])))
+def test_a_wait_that_gives_up_leaves_what_it_has_not_computed(spec):
+    """At 1 ns every CTA's first wait gives up, and nothing is written; at a few microseconds some of them do, and
+    what is written is right.  The call says so, and the next one is whole again."""
+    c = Case(*spec).device()
+    c.run()
+    o, lse = c.o.clone(), c.lse.clone()
+    acc0 = torch.rand(c.B, c.Hkv, c.S, generator=torch.Generator().manual_seed(2)).cuda()
+
+    def weights():
+        acc = acc0.clone()
+        fr.fr_attention_weights(ptr(c.dq), ptr(c.dk), ptr(lse), ptr(c.dlens), ptr(c.dwords), 0, ptr(acc), c.B, c.Hq, c.Hkv, c.N, c.S,
+                                c.dh, stream())
+        return acc
+
+    acc = weights()
+    assert fr.fr_ops_sync_status(stream()) == 0
+
+    def gave_up(codes):
+        try:
+            return fr.fr_ops_sync_status(stream())
+        except fr.FrError as e:
+            assert e.code == fr.FR_ERR_TIMEOUT and any(f"0x{x:08x}" in str(e) for x in codes), e
+            return e.code
+
+    marks = torch.full_like(o, MARK), torch.full_like(lse, MARK)
+    try:
+        for limit in (1, 300, 1000, 2000, 4000, 8000, 16000, 1):
+            fr.fr_ops_set_wait_limit(limit)
+            c.o.fill_(MARK), c.lse.fill_(MARK)
+            c.run()
+            rc = gave_up((0x710, 0x711, 0x713))
+            if limit == 1:
+                assert rc == fr.FR_ERR_TIMEOUT and torch.equal(c.o, marks[0]) and torch.equal(c.lse, marks[1])
+            elif rc == 0:
+                assert torch.equal(c.o, o) and torch.equal(c.lse, lse)
+            assert bool(((c.o == o) | (c.o == MARK)).all()) and bool(((c.lse == lse) | (c.lse == MARK)).all())
+            got = weights()
+            rc = gave_up((0x720, 0x721, 0x723))
+            if limit == 1:
+                assert rc == fr.FR_ERR_TIMEOUT and torch.equal(got, acc0)
+            elif rc == 0:
+                assert torch.equal(got, acc)
+            assert bool(((got == acc) | (got == acc0)).all())
+    finally:
+        fr.fr_ops_set_wait_limit(0)
+    c.run()
+    assert torch.equal(c.o, o) and torch.equal(c.lse, lse) and torch.equal(weights(), acc)
+    assert fr.fr_ops_sync_status(stream()) == 0

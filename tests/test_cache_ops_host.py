@@ -137,3 +137,10 @@ def test_attention_scratch(abi):
     if n:
         for scratch, size in ((None, n), (A, n - 1)):
             assert lib.fr_attention_tree(A, A, A, A, A, A, A, 1, 8, 1, 4, 1000, 128, scratch, size, None) == abi.FR_ERR_SHAPE
+
+
+def test_wait_limit_refused(abi):
+    with pytest.raises(abi.FrError) as e:
+        abi.fr_ops_set_wait_limit(10 ** 10 + 1)
+    assert e.value.code == abi.FR_ERR_ARG
+    abi.fr_ops_set_wait_limit(0)
