@@ -2,6 +2,7 @@
 // drafted tokens, eviction.  Argument checks here, kernels in tree_attention.cu and cache_moves.cu.
 #include <atomic>
 #include <cmath>
+#include <mutex>
 
 #include <cuda.h>
 
@@ -49,6 +50,21 @@ int check_pointers(const char* op, const void* const* ptrs, int n) {
     return FR_ERR_ARG;
   }
   return FR_OK;
+}
+
+// Before a launch: the ops' status word, and the attributes of the cache ops' kernels, set by the first cache op on
+// each device (no other op needs them, or fails with them).
+constexpr int MAX_DEVICES = 64;
+std::once_flag g_init_once[MAX_DEVICES];
+cudaError_t g_init_err[MAX_DEVICES];
+
+cudaError_t cache_op_begin(unsigned** status) {
+  int dev = 0;
+  const cudaError_t e = ops_status_word(status, &dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= MAX_DEVICES) return cudaErrorInvalidDevice;
+  std::call_once(g_init_once[dev], [dev] { g_init_err[dev] = tc::cache_ops_init(); });
+  return g_init_err[dev];
 }
 
 std::atomic<uint64_t> g_wait_ns{tc::WAIT_LIMIT_NS};
@@ -157,7 +173,7 @@ int fr_attention_tree(const void* q, const void* k, const void* v, const int32_t
   const void* ptrs[] = {q, k, v, lens, mask, o, lse, need > 0 ? scratch : nullptr};
   if ((rc = check_pointers(op, ptrs, 8))) return rc;
   tc::TreeArgs a{};
-  FR_CUDA(ops_status_word(&a.status, nullptr));
+  FR_CUDA(cache_op_begin(&a.status));
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k = static_cast<const __nv_bfloat16*>(k);
   a.v = static_cast<const __nv_bfloat16*>(v);
@@ -187,7 +203,7 @@ int fr_attention_weights(const void* q, const void* k, const float* lse, const i
   const void* ptrs[] = {q, k, lse, lens, mask, use, acc};
   if ((rc = check_pointers(op, ptrs, 7))) return rc;
   tc::TreeArgs a{};
-  FR_CUDA(ops_status_word(&a.status, nullptr));
+  FR_CUDA(cache_op_begin(&a.status));
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k = static_cast<const __nv_bfloat16*>(k);
   a.lens = lens;
@@ -229,7 +245,7 @@ int fr_cache_commit(void* k, void* v, float* acc, int32_t* pos, const int32_t* l
   const void* ptrs[] = {k, v, acc, pos, lens, path, npath, lens_out};
   if ((rc = check_pointers(op, ptrs, 8))) return rc;
   tc::MoveArgs a{};
-  FR_CUDA(ops_status_word(&a.status, nullptr));
+  FR_CUDA(cache_op_begin(&a.status));
   a.k = static_cast<uint8_t*>(k);
   a.v = static_cast<uint8_t*>(v);
   a.acc = acc;
@@ -271,7 +287,7 @@ int fr_cache_evict(void* k, void* v, const float* acc, const int32_t* pos, const
   const void* ptrs[] = {k, v, acc, pos, lens, acc_out, pos_out, lens_out, src};
   if ((rc = check_pointers(op, ptrs, 9))) return rc;
   tc::MoveArgs a{};
-  FR_CUDA(ops_status_word(&a.status, nullptr));
+  FR_CUDA(cache_op_begin(&a.status));
   a.k = static_cast<uint8_t*>(k);
   a.v = static_cast<uint8_t*>(v);
   a.acc_in = acc;

@@ -10,7 +10,7 @@
 
 namespace fr {
 
-// Device address of the ops' status word on the current device (ops.cu).
+// Device address of the ops' status word on the current device, looked up once per device (ops.cu).
 cudaError_t ops_status_word(unsigned** out, int* dev_out);
 
 namespace tc {
@@ -58,7 +58,7 @@ struct MoveArgs {
 };
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // tc_kernels.cu
-cudaError_t cache_ops_init();   // kernel attributes, once per device
+cudaError_t cache_ops_init();   // attributes of the cache ops' kernels on the current device
 size_t tree_scratch_bytes(int B, int Hq, int Hkv, int N, int S_max, int dh);
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);
 cudaError_t launch_attention_weights(const TreeArgs& a, cudaStream_t s);

@@ -26,10 +26,7 @@ cudaError_t ensure_tc_kernels(int* dev_out) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= MAX_DEVICES) return cudaErrorInvalidDevice;
-  std::call_once(g_init_once[dev], [dev] {
-    g_init_err[dev] = tc::tc_kernels_init();
-    if (g_init_err[dev] == cudaSuccess) g_init_err[dev] = tc::cache_ops_init();
-  });
+  std::call_once(g_init_once[dev], [dev] { g_init_err[dev] = tc::tc_kernels_init(); });
   if (dev_out) *dev_out = dev;
   return g_init_err[dev];
 }
@@ -46,11 +43,11 @@ cudaError_t g_status_err[MAX_DEVICES];
 
 }  // namespace
 
-// Device address of the ops' status word on the current device (kernel attributes set too).
 cudaError_t ops_status_word(unsigned** out, int* dev_out) {
   int dev = 0;
-  cudaError_t e = ensure_tc_kernels(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= MAX_DEVICES) return cudaErrorInvalidDevice;
   std::call_once(g_status_once[dev], [dev] {
     void* p = nullptr;
     g_status_err[dev] = cudaGetSymbolAddress(&p, g_ops_status);
@@ -132,6 +129,7 @@ int fr_attention(const void* q, const void* k, const void* v, void* o, int B, in
     return FR_ERR_SHAPE;
   }
   unsigned* status = nullptr;
+  FR_CUDA(ensure_tc_kernels(nullptr));
   FR_CUDA(ops_status_word(&status, nullptr));
   const tc::AttnArgs a = attention_args(q, k, v, o, B, Hq, Hkv, H, S_keys, dh, static_cast<float*>(scratch), status);
   FR_CUDA(tc::launch_attention_tc(a, B, reinterpret_cast<cudaStream_t>(stream), false));
@@ -189,6 +187,7 @@ extern "C" int fr_attention_noalloc(const void* q, const void* k, const void* v,
   }
   int dev = 0;
   unsigned* status = nullptr;
+  FR_CUDA(ensure_tc_kernels(nullptr));
   FR_CUDA(ops_status_word(&status, &dev));
   // once per device, with that device current: the array's device address
   std::call_once(g_noalloc_once[dev], [dev] {
