@@ -57,13 +57,15 @@ int check_pointers(const char* op, const void* const* ptrs, int n) {
 constexpr int MAX_DEVICES = 64;
 std::once_flag g_init_once[MAX_DEVICES];
 cudaError_t g_init_err[MAX_DEVICES];
+int g_tree_regs[MAX_DEVICES];   // not 0: refused, see cache_ops_init
 
-cudaError_t cache_op_begin(unsigned** status) {
+cudaError_t cache_op_begin(unsigned** status, int* tree_regs = nullptr) {
   int dev = 0;
   const cudaError_t e = ops_status_word(status, &dev);
   if (e != cudaSuccess) return e;
   if (dev >= MAX_DEVICES) return cudaErrorInvalidDevice;
-  std::call_once(g_init_once[dev], [dev] { g_init_err[dev] = tc::cache_ops_init(); });
+  std::call_once(g_init_once[dev], [dev] { g_init_err[dev] = tc::cache_ops_init(&g_tree_regs[dev]); });
+  if (tree_regs) *tree_regs = g_tree_regs[dev];
   return g_init_err[dev];
 }
 
@@ -173,7 +175,12 @@ int fr_attention_tree(const void* q, const void* k, const void* v, const int32_t
   const void* ptrs[] = {q, k, v, lens, mask, o, lse, need > 0 ? scratch : nullptr};
   if ((rc = check_pointers(op, ptrs, 8))) return rc;
   tc::TreeArgs a{};
-  FR_CUDA(cache_op_begin(&a.status));
+  int regs = 0;
+  FR_CUDA(cache_op_begin(&a.status, &regs));
+  if (regs) {
+    set_error("%s: this build's kernel has %d registers a thread, which its register moves do not add up to", op, regs);
+    return FR_ERR_UNSUPPORTED;
+  }
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k = static_cast<const __nv_bfloat16*>(k);
   a.v = static_cast<const __nv_bfloat16*>(v);

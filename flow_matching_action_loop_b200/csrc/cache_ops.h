@@ -58,7 +58,9 @@ struct MoveArgs {
 };
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // tc_kernels.cu
-cudaError_t cache_ops_init();   // attributes of the cache ops' kernels on the current device
+// Attributes of the cache ops' kernels on the current device; *regs becomes the attention kernel's registers per
+// thread where these are not what its register moves need.
+cudaError_t cache_ops_init(int* regs);
 size_t tree_scratch_bytes(int B, int Hq, int Hkv, int N, int S_max, int dh);
 cudaError_t launch_tree_attention(const TreeArgs& a, cudaStream_t s);
 cudaError_t launch_attention_weights(const TreeArgs& a, cudaStream_t s);

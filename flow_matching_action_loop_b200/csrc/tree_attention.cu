@@ -58,7 +58,8 @@ using namespace fr::sm100;
 constexpr int TA_SOFTMAX = 256;                // softmax threads
 constexpr int TA_THREADS = TA_SOFTMAX + 128;   // + a warpgroup of the copy warp and the MMA warp
 // Registers: 384 threads are launched with 168 each; a softmax thread holds a row's 128 scores, so that the
-// score buffer is free as soon as they are loaded.
+// score buffer is free as soon as they are loaded.  (setmaxnreg draws on what the block was launched with: compiled to
+// fewer registers, the growing warpgroups would wait for good.  tree_init refuses such a build.)
 constexpr int TA_REGS = 168, TA_REGS_SOFTMAX = 208, TA_REGS_OTHER = 88;
 static_assert(2 * TA_REGS_SOFTMAX + TA_REGS_OTHER == 3 * TA_REGS, "registers are only moved");
 constexpr int TA_CTAS = 148;                   // at most: the scratch holds two segments' rows for each
@@ -860,9 +861,15 @@ constexpr int MAX_DEVICES = 64;
 int g_clusters[MAX_DEVICES][3][TA_CLUSTER + 1];
 
 template <int DH>
-cudaError_t tree_init(int* clusters) {
+cudaError_t tree_init(int* clusters, int* regs) {
   const auto smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e = cudaFuncSetAttribute(k_tree_attn<DH, false>, smem, TreeGeom<DH>::smem);
+  cudaError_t e = cudaSuccess;
+  for (auto f : {k_tree_attn<DH, false>, k_tree_attn<DH, true>}) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, f)) != cudaSuccess) return e;
+    if (fa.numRegs != TA_REGS) *regs = fa.numRegs;
+  }
+  e = cudaFuncSetAttribute(k_tree_attn<DH, false>, smem, TreeGeom<DH>::smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k_tree_attn<DH, true>, smem, TreeGeom<DH>::smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k_tree_attn<DH, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   for (int c = 2; e == cudaSuccess && c <= TA_CLUSTER; ++c) {
@@ -918,12 +925,13 @@ cudaError_t launch_tree_attention(const TreeArgs& args, cudaStream_t s) {
   return a.dh == 64 ? launch_tree<64>(a, s) : a.dh == 128 ? launch_tree<128>(a, s) : launch_tree<256>(a, s);
 }
 
-cudaError_t cache_ops_init() {
+cudaError_t cache_ops_init(int* regs) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev >= MAX_DEVICES) return e;
-  if ((e = tree_init<64>(g_clusters[dev][0])) != cudaSuccess || (e = tree_init<128>(g_clusters[dev][1])) != cudaSuccess ||
-      (e = tree_init<256>(g_clusters[dev][2])) != cudaSuccess)
+  if ((e = tree_init<64>(g_clusters[dev][0], regs)) != cudaSuccess ||
+      (e = tree_init<128>(g_clusters[dev][1], regs)) != cudaSuccess ||
+      (e = tree_init<256>(g_clusters[dev][2], regs)) != cudaSuccess)
     return e;
   if ((e = weights_init()) != cudaSuccess) return e;
   return cache_moves_init();

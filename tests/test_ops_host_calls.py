@@ -81,3 +81,16 @@ for name, op in cache_ops.items():
 assert lib.fake_launches() == 1
 assert fr.fr_ops_sync_status() == 0 and attention()[0] == 0
 ''')
+
+
+@pytest.mark.parametrize("registers", [160, 176])
+def test_attention_tree_refuses_a_build_whose_registers_do_not_add_up(library, registers):
+    """Its kernel moves registers between warpgroups and would wait for good; nothing is launched."""
+    child(library, f'''
+lib.fake_registers({registers})
+for _ in range(2):
+    rc, text = cache_ops["tree"]()
+    assert rc == fr.FR_ERR_UNSUPPORTED and "{registers} registers" in text, (rc, text)
+assert lib.fake_launches() == 0
+assert cache_ops["weights"]()[0] == 0 and cache_ops["commit"]()[0] == 0 and cache_ops["evict"]()[0] == 0
+''')
