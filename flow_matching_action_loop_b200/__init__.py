@@ -20,7 +20,7 @@ from ._abi import (  # noqa: F401
     DTYPES, FR_DTYPE_BF16, FR_DTYPE_F32, FR_DTYPE_FP8, FR_DTYPE_W4A16, FR_ERR_ARG, FR_ERR_CUDA, FR_ERR_DEVICE, FR_ERR_SHAPE,
     FR_ERR_STATE, FR_ERR_TIMEOUT, FR_ERR_UNSUPPORTED, FR_OK, FR_PATH_AUTO, FR_PATH_STEPWISE, FR_PATH_TENSOR,
     FR_EXEC_AUTO, FR_EXEC_GRAPH, FR_EXEC_PERSISTENT, fr_set_exec_mode, fr_exec_mode, fr_set_wait_limit,
-    fr_device_checks, fr_debug_limit_extent,
+    fr_device_checks, fr_debug_limit_extent, fr_debug_limit_op_extent,
     FR_ATTENTION_NOALLOC_SCRATCH_BYTES, FR_CACHE_MAX_SLOTS, FR_CAPSULE_MAGIC, FR_EVICT_MAX_SLOTS, FR_TREE_MAX_NODES,
     fr_attention_tree, fr_attention_tree_scratch_bytes, fr_attention_weights, fr_cache_commit, fr_cache_evict,
     fr_tree_mask, fr_ops_set_wait_limit, FR_PREFIX_K_ROTATED, FrCapsule, FrConfig, FrError,

@@ -120,6 +120,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "fr_ops_sync_status": (c_int, [c_void_p]),
         "fr_attention_noalloc": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
                                          c_int, c_void_p]),
+        "fr_debug_limit_op_extent": (c_int, [c_char_p, ctypes.c_uint64]),
         "fr_ops_set_wait_limit": (c_int, [ctypes.c_uint64]),
         "fr_tree_mask": (c_int, [ctypes.POINTER(ctypes.c_int32), c_int, ctypes.POINTER(ctypes.c_uint32)]),
         "fr_attention_tree": (c_int, [c_void_p] * 7 + [c_int] * 6 + [c_void_p, ctypes.c_size_t, c_void_p]),
@@ -384,6 +385,10 @@ def fr_attention_noalloc(q: int, k: int, v: int, o: int, B: int, Hq: int, Hkv: i
 
 
 FR_TREE_MAX_NODES, FR_CACHE_MAX_SLOTS, FR_EVICT_MAX_SLOTS = 256, 1 << 24, 1 << 19
+
+
+def fr_debug_limit_op_extent(buffer: str, elems: int) -> None:
+    _check(load_library().fr_debug_limit_op_extent(buffer.encode(), int(elems)), "fr_debug_limit_op_extent")
 
 
 def fr_ops_set_wait_limit(limit_ns: int) -> None:

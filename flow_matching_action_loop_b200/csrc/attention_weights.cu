@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
           const float2 wp = unpack_f32x2(add_f32x2(w2[0], w2[1]));
           const float w = so_far + (wp.x + wp.y);
           if (MANY && !last) *part = w;
-          if (last && slot < keys && !*abort_v) acc[slot] = (slot < len ? before : 0.f) + w;
+          if (last && slot < keys && !*abort_v && in_bounds(a.status, acc - a.acc + slot, a.ext.acc, CHK_WEIGHTS_ACC))
+            acc[slot] = (slot < len ? before : 0.f) + w;
           before = next;
         }
       }

@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(CM_THREADS) k_cache_commit(const __grid_consta
   __shared__ int path[CM_THREADS];   // N <= FR_TREE_MAX_NODES
   const int part = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int len = a.lens[b], np = a.npath[b];
-  const bool writer = part == 0 && h == 0 && tid == 0;
+  const bool writer = part == 0 && h == 0 && tid == 0 && in_bounds(a.status, b, a.ext.lens, CHK_COMMIT_LENS);
   if (len < 0) {
     if (writer) a.lens_out[b] = len;
     return;
@@ -50,7 +50,8 @@ __global__ void __launch_bounds__(CM_THREADS) k_cache_commit(const __grid_consta
   uint32_t w = 0;
   if (word && tid < np) w = word[slot0 + path[tid]];
   __syncthreads();
-  if (word && tid < np) word[slot0 + tid] = w;
+  if (word && tid < np && in_bounds(a.status, slot0 + tid, part == 0 ? a.ext.acc : a.ext.pos, CHK_COMMIT_SLOTS))
+    word[slot0 + tid] = w;
   const int nv = a.row_bytes / 16;
   uint4* rows = reinterpret_cast<uint4*>(part == 0 ? a.k : a.v) + slot0 * nv;
   const int per = CM_THREADS * CM_VECS / nv;   // rows per round
@@ -66,7 +67,8 @@ __global__ void __launch_bounds__(CM_THREADS) k_cache_commit(const __grid_consta
 #pragma unroll
     for (int u = 0; u < CM_VECS; ++u) {
       const int it = tid + u * CM_THREADS;
-      if (it < items) rows[static_cast<size_t>(i0) * nv + it] = x[u];
+      const size_t to = static_cast<size_t>(i0) * nv + it;
+      if (it < items && in_bounds(a.status, slot0 * nv + to, a.ext.rows, CHK_COMMIT_ROWS)) rows[to] = x[u];
     }
   }
 }
@@ -114,7 +116,14 @@ __global__ void __launch_bounds__(EV_THREADS, 2) k_cache_evict(const __grid_cons
   float* acc_out = a.acc_out + row0;
   int32_t* pos_out = a.pos_out + row0;
   int32_t* src = a.src + (static_cast<size_t>(b) * a.Hkv + h) * keep;
-  const bool writer = h == 0 && c == 0 && tid == 0;
+  const bool writer = h == 0 && c == 0 && tid == 0 && in_bounds(a.status, b, a.ext.lens, CHK_EVICT_LENS);
+  auto put_src = [&](int j, int v) {
+    if (in_bounds(a.status, src - a.src + j, a.ext.src, CHK_EVICT_SRC)) src[j] = v;
+  };
+  auto put_slot = [&](int j, float w, int32_t q) {
+    if (in_bounds(a.status, row0 + j, a.ext.acc, CHK_EVICT_SLOTS)) acc_out[j] = w;
+    if (in_bounds(a.status, row0 + j, a.ext.pos, CHK_EVICT_SLOTS)) pos_out[j] = q;
+  };
   if (len < 0 || len > a.S_max) {   // the whole cluster leaves
     if (writer) {
       if (len > a.S_max) report_sample(a.status, CACHE_BAD_LEN, b);
@@ -125,11 +134,8 @@ __global__ void __launch_bounds__(EV_THREADS, 2) k_cache_evict(const __grid_cons
   if (writer) a.lens_out[b] = min(len, keep);
   if (len <= keep) {   // nothing to free
     for (int j = c * EV_THREADS + tid; j < keep; j += C * EV_THREADS) {
-      src[j] = j < len ? j : -1;
-      if (j < len) {
-        acc_out[j] = acc[j];
-        pos_out[j] = pos[j];
-      }
+      put_src(j, j < len ? j : -1);
+      if (j < len) put_slot(j, acc[j], pos[j]);
     }
     return;
   }
@@ -155,9 +161,8 @@ __global__ void __launch_bounds__(EV_THREADS, 2) k_cache_evict(const __grid_cons
     pm = max(pm, q);
     if (in) key[i] = k;
     if (in && lo + i < keep) {   // as if it stayed; a freed slot's new token overwrites this
-      src[lo + i] = lo + i;
-      acc_out[lo + i] = w;
-      pos_out[lo + i] = q;
+      put_src(lo + i, lo + i);
+      put_slot(lo + i, w, q);
     }
   }
   if (a.recent > 0) {
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(EV_THREADS, 2) k_cache_evict(const __grid_cons
       const int s = cm * per + cl.map_shared_rank(list, cm)[per - 1 - (r - move_base[cm])];
       mv_dst[tid] = dst;
       mv_src[tid] = s;
-      src[dst] = s;
+      put_src(dst, s);
       w = acc[s];   // stored behind the rows
       q = pos[s];
     }
@@ -357,13 +362,13 @@ __global__ void __launch_bounds__(EV_THREADS, 2) k_cache_evict(const __grid_cons
           if (m0 + u * EV_WARPS < nb) x[u] = base[static_cast<size_t>(mv_src[m0 + u * EV_WARPS]) * nv];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (m0 + u * EV_WARPS < nb) base[static_cast<size_t>(mv_dst[m0 + u * EV_WARPS]) * nv] = x[u];
+          if (m0 + u * EV_WARPS < nb) {
+            const size_t to = static_cast<size_t>(mv_dst[m0 + u * EV_WARPS]) * nv;
+            if (in_bounds(a.status, row0 * nv + to + (e < nv ? e : e - nv), a.ext.rows, CHK_EVICT_ROWS)) base[to] = x[u];
+          }
       }
     }
-    if (tid < nb) {
-      acc_out[dst] = w;
-      pos_out[dst] = q;
-    }
+    if (tid < nb) put_slot(dst, w, q);
     __syncthreads();
   }
   cl.sync();   // no CTA leaves while another reads its lists

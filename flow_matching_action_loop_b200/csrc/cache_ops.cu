@@ -2,6 +2,7 @@
 // drafted tokens, eviction.  Argument checks here, kernels in tree_attention.cu and cache_moves.cu.
 #include <atomic>
 #include <cmath>
+#include <cstring>
 #include <mutex>
 
 #include <cuda.h>
@@ -71,6 +72,20 @@ cudaError_t cache_op_begin(unsigned** status, int* tree_regs = nullptr) {
 
 std::atomic<uint64_t> g_wait_ns{tc::WAIT_LIMIT_NS};
 
+// Extents of a call's buffers, or smaller ones declared for a test of the checks (fr_debug_limit_op_extent).
+const char* const EXTENT_NAMES[] = {"o", "lse", "scratch", "acc", "pos", "src", "lens", "rows"};
+std::atomic<uint64_t> g_extent_limit[8];
+
+tc::CacheExtents extents(uint64_t o, uint64_t lse, uint64_t scratch, uint64_t slots, uint64_t src, uint64_t lens,
+                         uint64_t rows) {
+  uint64_t e[8] = {o, lse, scratch, slots, slots, src, lens, rows};
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t limit = g_extent_limit[i].load(std::memory_order_relaxed);
+    if (limit && limit < e[i]) e[i] = limit;
+  }
+  return {e[0], e[1], e[2], e[3], e[4], e[5], e[6], e[7]};
+}
+
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 int check_tree_sizes(const char* op, int B, int Hq, int Hkv, int N, int S_max, int dh) {
@@ -126,6 +141,24 @@ int fr_ops_set_wait_limit(uint64_t limit_ns) {
   }
   g_wait_ns = limit_ns ? limit_ns : tc::WAIT_LIMIT_NS;
   return FR_OK;
+}
+
+int fr_debug_limit_op_extent(const char* buffer, uint64_t elems) {
+  if (!buffer) {
+    set_error("fr_debug_limit_op_extent: NULL argument");
+    return FR_ERR_ARG;
+  }
+  if (!fr_device_checks()) {
+    set_error("fr_debug_limit_op_extent: this library was built without device bounds checks");
+    return FR_ERR_UNSUPPORTED;
+  }
+  for (int i = 0; i < 8; ++i)
+    if (!std::strcmp(buffer, EXTENT_NAMES[i])) {
+      g_extent_limit[i] = elems;
+      return FR_OK;
+    }
+  set_error("fr_debug_limit_op_extent: no buffer \"%s\"", buffer);
+  return FR_ERR_ARG;
 }
 
 int fr_tree_mask(const int32_t* parents, int n, uint32_t* mask) {
@@ -192,6 +225,8 @@ int fr_attention_tree(const void* q, const void* k, const void* v, const int32_t
   a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.N = N, a.W = (N + 31) / 32, a.S_max = S_max, a.dh = dh;
   a.scale = 1.0f / std::sqrt(static_cast<float>(dh));
   a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  const uint64_t rows = static_cast<uint64_t>(B) * Hq * N;
+  a.ext = extents(rows * dh, rows, need / 4, 0, 0, 0, 0);
   FR_CUDA(tc::launch_tree_attention(a, reinterpret_cast<cudaStream_t>(stream)));
   return FR_OK;
 }
@@ -221,6 +256,7 @@ int fr_attention_weights(const void* q, const void* k, const float* lse, const i
   a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.N = N, a.W = (N + 31) / 32, a.S_max = S_max, a.dh = dh;
   a.scale = 1.0f / std::sqrt(static_cast<float>(dh));
   a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  a.ext = extents(0, 0, 0, static_cast<uint64_t>(B) * Hkv * S_max, 0, 0, 0);
   FR_CUDA(tc::launch_attention_weights(a, reinterpret_cast<cudaStream_t>(stream)));
   return FR_OK;
 }
@@ -262,6 +298,8 @@ int fr_cache_commit(void* k, void* v, float* acc, int32_t* pos, const int32_t* l
   a.npath = npath;
   a.lens_out = lens_out;
   a.B = B, a.Hkv = Hkv, a.N = N, a.S_max = S_max, a.row_bytes = dh * (dtype == FR_DTYPE_F32 ? 4 : 2);
+  const uint64_t slots = static_cast<uint64_t>(B) * Hkv * S_max;
+  a.ext = extents(0, 0, 0, slots, 0, B, slots * a.row_bytes / 16);
   FR_CUDA(tc::launch_cache_commit(a, reinterpret_cast<cudaStream_t>(stream)));
   return FR_OK;
 }
@@ -306,6 +344,8 @@ int fr_cache_evict(void* k, void* v, const float* acc, const int32_t* pos, const
   a.src = src;
   a.B = B, a.Hkv = Hkv, a.S_max = S_max, a.row_bytes = dh * (dtype == FR_DTYPE_F32 ? 4 : 2);
   a.keep = keep, a.recent = recent;
+  const uint64_t slots = static_cast<uint64_t>(B) * Hkv * S_max;
+  a.ext = extents(0, 0, 0, slots, static_cast<uint64_t>(B) * Hkv * keep, B, slots * a.row_bytes / 16);
   FR_CUDA(tc::launch_cache_evict(a, reinterpret_cast<cudaStream_t>(stream)));
   return FR_OK;
 }

@@ -18,6 +18,16 @@ namespace tc {
 // where-codes of the samples that the cache ops refuse (fr_ops_sync_status)
 constexpr uint32_t CACHE_BAD_LEN = 0xC001u, CACHE_BAD_PATH = 0xC002u;
 
+// Extents of the buffers that the cache ops store into, in elements of each (rows: 16-byte words of K or of V), and
+// the where-codes of their checks.  Checked builds verify every store against them; the product build carries them
+// unused.
+struct CacheExtents {
+  uint64_t o, lse, scratch, acc, pos, src, lens, rows;
+};
+constexpr uint32_t CHK_TREE_O = 0x9020u, CHK_TREE_LSE = 0x9021u, CHK_TREE_SCRATCH = 0x9022u, CHK_WEIGHTS_ACC = 0x9030u,
+                   CHK_COMMIT_ROWS = 0x9040u, CHK_COMMIT_SLOTS = 0x9041u, CHK_COMMIT_LENS = 0x9042u,
+                   CHK_EVICT_ROWS = 0x9050u, CHK_EVICT_SLOTS = 0x9051u, CHK_EVICT_SRC = 0x9052u, CHK_EVICT_LENS = 0x9053u;
+
 struct TreeArgs {
   const __nv_bfloat16* q;      // [B][Hq][N][dh]
   const __nv_bfloat16* k;      // [B][Hkv][S_max][dh]
@@ -36,6 +46,7 @@ struct TreeArgs {
   int rtg, groups;             // CTAs per group (row tiles of a unit), groups that share the tiles
   int whole_extra;             // tiles that keeping a unit whole may cost a group
   int cluster;                 // attention: CTAs of a unit's cluster, 1: none
+  CacheExtents ext;
   CUtensorMap tm_q, tm_k, tm_v;   // written by the launchers
 };
 
@@ -55,6 +66,7 @@ struct MoveArgs {
   int32_t* src;                // evict: [B][Hkv][keep]
   unsigned* status;
   int B, Hkv, N, S_max, row_bytes, keep, recent;
+  CacheExtents ext;
 };
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // tc_kernels.cu

@@ -129,9 +129,10 @@ struct MergedRow {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
-    st_global_32(a.o + ((static_cast<size_t>(b) * a.N + tok) * a.Hq + hq) * dh + fg * 16, w);
-    if (a.lse && fg == 0)
-      a.lse[(static_cast<size_t>(b) * a.Hq + hq) * a.N + tok] = row_lse(m, l);
+    const size_t at = ((static_cast<size_t>(b) * a.N + tok) * a.Hq + hq) * dh + fg * 16;
+    if (in_bounds(a.status, at + 15, a.ext.o, CHK_TREE_O)) st_global_32(a.o + at, w);
+    const size_t at_lse = (static_cast<size_t>(b) * a.Hq + hq) * a.N + tok;
+    if (a.lse && fg == 0 && in_bounds(a.status, at_lse, a.ext.lse, CHK_TREE_LSE)) a.lse[at_lse] = row_lse(m, l);
   }
 };
 
@@ -591,6 +592,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
 #pragma unroll 1
         for (int c0 = hh * (DH / 2); c0 < (hh + 1) * (DH / 2); c0 += 32) {
           uint32_t ov[32];
+          __syncwarp();   // (rows that store nothing)
           tmem_ld32_nowait(tO + lanes + c0, ov);
           tmem_wait_ld();
           if (!mine || (!CL && whole && *abort_v)) continue;
@@ -601,24 +603,29 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 w[i] = pack_bf16x2(__uint_as_float(ov[e + 2 * i]) * inv, __uint_as_float(ov[e + 2 * i + 1]) * inv);
-              st_global_32(orow + c0 + e, w);
+              if (in_bounds(a.status, orow - a.o + c0 + e + 15, a.ext.o, CHK_TREE_O)) st_global_32(orow + c0 + e, w);
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(part + static_cast<size_t>((c0 + e) / 4) * RW * 4) =
-                  make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+            for (int e = 0; e < 32; e += 4) {
+              float* at = part + static_cast<size_t>((c0 + e) / 4) * RW * 4;
+              if (CL || in_bounds(a.status, at - a.scratch + 3, a.ext.scratch, CHK_TREE_SCRATCH))
+                *reinterpret_cast<uint4*>(at) = make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+            }
           }
         }
         tc_fence_before();
         pair_barrier(pw);   // both groups have read O and the sums before either goes on
         if (mine && hh == 0) {
           const bool lost = *abort_v != 0;   // then what either group has read may be wrong, or was left out
+          const size_t at_lse = (static_cast<size_t>(it.b) * a.Hq + hq) * a.N + tok;
           if (!whole) {
-            *reinterpret_cast<float4*>(part + static_cast<size_t>(DH / 4) * RW * 4) =
-                make_float4(!CL && lost ? NAN : ref, CL ? copysignf(lt, bad_v != bad_v ? -1.f : 1.f) : lt, bad_v, 0.f);
-          } else if (a.lse && !lost) {
-            a.lse[(static_cast<size_t>(it.b) * a.Hq + hq) * a.N + tok] = row_lse(ref, lt);
+            float* at = part + static_cast<size_t>(DH / 4) * RW * 4;
+            if (CL || in_bounds(a.status, at - a.scratch + 3, a.ext.scratch, CHK_TREE_SCRATCH))
+              *reinterpret_cast<float4*>(at) =
+                  make_float4(!CL && lost ? NAN : ref, CL ? copysignf(lt, bad_v != bad_v ? -1.f : 1.f) : lt, bad_v, 0.f);
+          } else if (a.lse && !lost && in_bounds(a.status, at_lse, a.ext.lse, CHK_TREE_LSE)) {
+            a.lse[at_lse] = row_lse(ref, lt);
           }
         }
       }
@@ -689,7 +696,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
         if (k < n) weight[k * 128 + tid] = st[k].x * inv;
       if (a.lse && me == 0 && n > 0 && !lost) {
         const int rr = u.rt * 128 + tid, hq = u.hk * g + rr / a.N;
-        a.lse[(static_cast<size_t>(u.b) * a.Hq + hq) * a.N + rr % a.N] = row_lse(m, l);
+        const size_t at = (static_cast<size_t>(u.b) * a.Hq + hq) * a.N + rr % a.N;
+        if (in_bounds(a.status, at, a.ext.lse, CHK_TREE_LSE)) a.lse[at] = row_lse(m, l);
       }
     }
     lost = __syncthreads_or(lost) != 0;
@@ -715,8 +723,9 @@ __global__ void __launch_bounds__(TA_THREADS, 1) k_tree_attn(const __grid_consta
           }
       }
       const int hq = u.hk * g + rr / a.N;
-      *reinterpret_cast<uint2*>(a.o + ((static_cast<size_t>(u.b) * a.N + rr % a.N) * a.Hq + hq) * DH + f4 * 4) =
-          make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+      const size_t at = ((static_cast<size_t>(u.b) * a.N + rr % a.N) * a.Hq + hq) * DH + f4 * 4;
+      if (in_bounds(a.status, at + 3, a.ext.o, CHK_TREE_O))
+        *reinterpret_cast<uint2*>(a.o + at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
     }
     // no CTA leaves while another reads its rows (the loads have returned: o has been stored)
     cluster_arrive_relaxed();

@@ -287,7 +287,7 @@ int fr_set_wait_limit(fr_handle* h, uint64_t limit_ns);
 /* ---- device bounds checks (checked builds) ---- */
 
 /* 1 if this library was built with device bounds checks (-DFR_DEVICE_CHECKS), else 0.  In a checked
- * build every store of the GEMM epilogues, of fr_attention's kernels and of the persistent kernel
+ * build every store of the GEMM epilogues, of the attention kernels, of the cache ops and of the persistent kernel
  * verifies its index against its buffer's extent; an index at or past it latches FR_ERR_DEVICE in the
  * status word (fr_sync_status / fr_ops_sync_status: where-code and index) and the store is skipped.
  * No counterpart in the pages: it stands in for a memory checker in debugging. */
@@ -312,6 +312,12 @@ int fr_debug_plan(const fr_config* cfg, int B, int P, int nsm, int max_dyn, int 
  * any access leaving the real allocation.  Cached graphs are dropped.  Errors: FR_ERR_ARG (NULL,
  * unknown name), FR_ERR_STATE (not a tensor-path handle), FR_ERR_UNSUPPORTED (not a checked build). */
 int fr_debug_limit_extent(fr_handle* h, const char* buffer, uint64_t elems);
+
+/* fr_debug_limit_op_extent -- the same for the cache ops, for the calls of this process from then on: buffers "o",
+ * "lse", "scratch" (fr_attention_tree; scratch in floats), "acc" and "pos" (slots: fr_attention_weights, and what
+ * fr_cache_commit and fr_cache_evict write of them), "src", "lens" (lens_out) and "rows" (16-byte words of K, and of
+ * V).  Errors: FR_ERR_ARG (NULL, unknown name), FR_ERR_UNSUPPORTED (not a checked build). */
+int fr_debug_limit_op_extent(const char* buffer, uint64_t elems);
 
 /*
  * fr_prefill -- the prefix pass, the step before the loop (FlashRT walkthrough, component 5:

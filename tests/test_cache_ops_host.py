@@ -144,3 +144,10 @@ def test_wait_limit_refused(abi):
         abi.fr_ops_set_wait_limit(10 ** 10 + 1)
     assert e.value.code == abi.FR_ERR_ARG
     abi.fr_ops_set_wait_limit(0)
+
+
+def test_declared_extents_need_the_checked_build(abi):
+    for name, code in (("o", abi.FR_ERR_UNSUPPORTED), ("rows", abi.FR_ERR_UNSUPPORTED)):
+        with pytest.raises(abi.FrError) as e:
+            abi.fr_debug_limit_op_extent(name, 10)
+        assert e.value.code == code
