@@ -899,16 +899,19 @@ cudaError_t tree_init(int* clusters, int* regs) {
 }
 
 // CTAs of a unit's cluster, or 1: tiles shared over the whole GPU.  A cluster is taken if all of them are
-// resident together and the longest sample's share per CTA is at most CLUSTER_EXTRA tiles above an equal
-// share of all tiles over the GPU: a tile takes about 0.6 us there, the merge kernel and a CTA's second
-// segment 4 us and more.
-constexpr int CLUSTER_EXTRA = 5;
+// resident together and a CTA's tiles, with every sample as long as the cache, are at most CLUSTER_EXTRA above an
+// equal share of all tiles over the GPU: a tile takes about 0.6 us there, the merge kernel and a CTA's second
+// segment 4 us and more.  The lengths are not known here: of one long sample among short ones a cluster's CTAs run
+// the same tiles, and the others idle.  So a CTA has at most CLUSTER_TILES.  Single tokens, 72 units of 256
+// features, us for clusters / shared tiles: 33 tiles (17 a CTA) 54 / 62 with all samples long, 36 / 26 with one, 44 /
+// 45 with lengths from an eighth on; 65 tiles 97 / 103, 62 / 38, 77 / 68; 258 tiles 353 / 356, 249 / 100, 264 / 230.
+constexpr int CLUSTER_EXTRA = 5, CLUSTER_TILES = 17;
 int tree_cluster(const int* resident, int ctas, int64_t units, int tiles) {
   int best = 1;
   for (int c = 2; c <= TA_CLUSTER && c <= tiles; ++c)
     if (units <= resident[c] && ((tiles + c - 1) / c < (tiles + best - 1) / best)) best = c;
   const int64_t share = units * tiles / ctas;
-  return best > 1 && (tiles + best - 1) / best <= share + CLUSTER_EXTRA ? best : 1;
+  return best > 1 && (tiles + best - 1) / best <= std::min<int64_t>(share + CLUSTER_EXTRA, CLUSTER_TILES) ? best : 1;
 }
 
 }  // namespace

@@ -9,7 +9,7 @@
 
 namespace {
 char fail_name[64];
-int fail_code, launches, registers = 168;
+int fail_code, launches, registers = 168, cluster = 1;
 alignas(256) char symbol[16 << 20];   // stands for every device symbol
 
 int result(const char* name) { return std::strcmp(name, fail_name) ? 0 : fail_code; }
@@ -30,6 +30,7 @@ void fake_fail(const char* name, int code) {
   fail_code = code;
 }
 int fake_launches() { return launches; }
+int fake_cluster() { return cluster; }   // of the last launch
 void fake_registers(int n) { registers = n; }
 
 void** __cudaRegisterFatBinary(void*) {
@@ -57,7 +58,7 @@ int cudaFuncGetAttributes(cudaFuncAttributes* a, const void*) {
   return result("cudaFuncGetAttributes");
 }
 int cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunchConfig_t* cfg) {
-  *n = 128 / static_cast<int>(cfg->gridDim.x);
+  *n = 148 / static_cast<int>(cfg->gridDim.x);
   return result("cudaOccupancyMaxActiveClusters");
 }
 int cudaOccupancyMaxActiveBlocksPerMultiprocessor(int* n) {
@@ -66,10 +67,14 @@ int cudaOccupancyMaxActiveBlocksPerMultiprocessor(int* n) {
 }
 int cudaLaunchKernel() {
   ++launches;
+  cluster = 1;
   return result("cudaLaunchKernel");
 }
-int cudaLaunchKernelExC() {
+int cudaLaunchKernelExC(const cudaLaunchConfig_t* cfg) {
   ++launches;
+  cluster = 1;
+  for (unsigned i = 0; i < cfg->numAttrs; ++i)
+    if (cfg->attrs[i].id == cudaLaunchAttributeClusterDimension) cluster = cfg->attrs[i].val.clusterDim.x;
   return result("cudaLaunchKernelExC");
 }
 int cudaGetSymbolAddress(void** p, const void*) {

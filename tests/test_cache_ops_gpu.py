@@ -896,3 +896,28 @@ def test_a_wait_that_gives_up_leaves_what_it_has_not_computed(spec):
     c.run()
     assert torch.equal(c.o, o) and torch.equal(c.lse, lse) and torch.equal(weights(), acc)
     assert fr.fr_ops_sync_status(stream()) == 0
+
+
+@pytest.mark.parametrize("spec", [
+    (8, 8, 1, 256, 5, 4000, [3900, 3, -1, 0, 60, -1, 7, 100], "tree"),                 # a cluster per unit
+    (9, 8, 1, 128, 1, 8300, [-1, 0, 1, 127, 8299, -1, 128, 2, 30], "chain"),
+    (74, 4, 1, 64, 3, 4100, [(b * 5) % 90 - 1 if b != 40 else 4097 for b in range(74)], "tree"),
+    (74, 4, 1, 64, 3, 12000, [(b * 5) % 90 - 1 if b != 73 else 11990 for b in range(74)], "tree"),   # more tiles than a cluster takes
+], ids=lambda s: "-".join(map(str, s[:6])))
+def test_one_long_sample_among_short_and_padded_ones(spec):
+    c = Case(*spec).device()
+    c.run()
+    o = c.oracle()
+    check(c, c.o, c.lse, o)
+    acc = torch.zeros(c.B, c.Hkv, c.S, device="cuda")
+    c.lse[torch.tensor(c.lens) < 0] = float("-inf")
+    fr.fr_attention_weights(ptr(c.dq), ptr(c.dk), ptr(c.lse), ptr(c.dlens), ptr(c.dwords), 0, ptr(acc), c.B, c.Hq, c.Hkv, c.N, c.S,
+                            c.dh, stream())
+    want, w = R.weigh(c.q.double().numpy(), c.k.double().numpy(), c.lse.double().cpu().numpy(), c.lens, c.words, None, np.zeros(acc.shape))
+    tl = c.dh * 2.0 ** -24 * o[3].max() + (8 + np.abs(np.where(np.isinf(o[2]), 0.0, o[2])).max()) * 2.0 ** -21
+    for b, n in enumerate(c.lens):
+        m = n + c.N if n >= 0 else 0
+        d = np.abs(acc[b, :, :m].cpu().numpy() - want[b, :, :m])
+        assert np.all(d <= w[b, :, :m] * (tl + c.Hq // c.Hkv * c.N * 2.0 ** -24) + 2.0 ** -24 * want[b, :, :m] + 1e-37)
+        assert float(acc[b, :, m:].abs().sum()) == 0.0
+    assert fr.fr_ops_sync_status(stream()) == 0

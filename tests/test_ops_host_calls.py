@@ -94,3 +94,14 @@ for _ in range(2):
 assert lib.fake_launches() == 0
 assert cache_ops["weights"]()[0] == 0 and cache_ops["commit"]()[0] == 0 and cache_ops["evict"]()[0] == 0
 ''')
+
+
+def test_attention_tree_takes_a_cluster_per_unit_only_for_few_tiles(library):
+    """Lengths are device data: a cluster's CTAs would run the tiles of one long sample alone while the others idle,
+    however short the others are.  (units, tiles of 128 slots) -> CTAs of a cluster, with 148 / c of them resident."""
+    child(library, r'''
+for units, tiles, want in ((1, 7, 7), (8, 17, 9), (9, 65, 13), (16, 65, 9), (74, 9, 2), (74, 33, 2), (74, 35, 1), (74, 258, 1), (72, 258, 1),
+                           (37, 65, 4), (37, 69, 1), (49, 51, 3), (49, 52, 1), (1, 129, 1), (200, 9, 1)):
+    rc, text = code(lambda: fr.fr_attention_tree(A, A, A, A, A, A, A, units, 8, 1, 1, tiles * 128, 128, A, 40 << 20))
+    assert rc == 0 and lib.fake_cluster() == want, (units, tiles, lib.fake_cluster(), text)
+''')
