@@ -921,3 +921,54 @@ def test_one_long_sample_among_short_and_padded_ones(spec):
         assert np.all(d <= w[b, :, :m] * (tl + c.Hq // c.Hkv * c.N * 2.0 ** -24) + 2.0 ** -24 * want[b, :, :m] + 1e-37)
         assert float(acc[b, :, m:].abs().sum()) == 0.0
     assert fr.fr_ops_sync_status(stream()) == 0
+
+
+@pytest.mark.parametrize("S,keep,recent,dtype", [(70, 10, 3, torch.float32), (3000, 1100, 0, torch.bfloat16), (9000, 9000, 64, torch.float32)])
+def test_evict_leaves_its_inputs_as_they_were(S, keep, recent, dtype):
+    """Bit for bit, NaN and zeros of both signs among the sums; sums and positions that stay keep their bits too."""
+    B, Hkv, dh, rng = 3, 2, 16, np.random.default_rng(S)
+    bits = rng.choice(np.array([0, 0x80000000, 0x7fc00000, 0xffc01234, 0x7f800000, 0xff800000, 1, 0x80000001, 0x3f800000], np.uint32), (B, Hkv, S))
+    acc, pos = torch.from_numpy(bits.view(np.float32)).cuda(), torch.from_numpy(rng.permutation(B * Hkv * S).astype(np.int32).reshape(B, Hkv, S)).cuda()
+    lens = torch.tensor([S, -1, S // 2], dtype=torch.int32).cuda()
+    k = torch.randn(B, Hkv, S, dh).to(dtype).cuda()
+    v, ins = k.clone(), [x.clone() for x in (acc.view(torch.int32), pos, lens)]
+    acc2, pos2, lens2 = torch.zeros_like(acc), torch.zeros_like(pos), torch.zeros_like(lens)
+    src = torch.zeros(B, Hkv, keep, dtype=torch.int32).cuda()
+    fr.fr_cache_evict(ptr(k), ptr(v), ptr(acc), ptr(pos), ptr(lens), ptr(acc2), ptr(pos2), ptr(lens2), ptr(src), B, Hkv, S, dh,
+                      fr.FR_DTYPE_F32 if dtype == torch.float32 else fr.FR_DTYPE_BF16, keep, recent, stream())
+    assert fr.fr_ops_sync_status(stream()) == 0
+    for x, y in zip((acc.view(torch.int32), pos, lens), ins):
+        assert torch.equal(x, y)
+    for b in (0, 2):
+        m = int(lens2[b])
+        for h in range(Hkv):
+            at = src[b, h, :m].long()
+            assert torch.equal(acc2[b, h, :m].view(torch.int32), ins[0][b, h][at]) and torch.equal(pos2[b, h, :m], ins[1][b, h][at])
+
+
+# one pass of rows, and several
+@pytest.mark.parametrize("spec", [(5, 4, 2, 64, 3, 100, [50, 97, 20, 4, -1], "tree"), (4, 8, 1, 256, 63, 700, [637, 100, 50, 0], "tree"),
+                                  (40, 8, 8, 128, 4, 300, [7 * b for b in range(40)], "chain")], ids=lambda s: "-".join(map(str, s[:6])))
+def test_attention_weights_refuse_bad_lengths_on_the_device(spec):
+    """lens + N past the cache, up to the largest int: those samples' sums stay as they were, the others' are right."""
+    c = Case(*spec).device()
+    c.run()
+    acc0 = torch.rand(c.B, c.Hkv, c.S, generator=torch.Generator().manual_seed(3)).cuda()
+
+    def weights():
+        acc = acc0.clone()
+        fr.fr_attention_weights(ptr(c.dq), ptr(c.dk), ptr(c.lse), ptr(c.dlens), ptr(c.dwords), 0, ptr(acc), c.B, c.Hq, c.Hkv, c.N, c.S,
+                                c.dh, stream())
+        return acc
+
+    want = weights()
+    assert fr.fr_ops_sync_status(stream()) == 0
+    bad = [0, 2, c.B - 2]
+    for b, n in zip(bad, (c.S - c.N + 1, 2 ** 31 - 1, c.S)):
+        c.dlens[b] = n
+        want[b] = acc0[b]
+    got = weights()
+    with pytest.raises(fr.FrError) as e:
+        fr.fr_ops_sync_status(stream())
+    assert e.value.code == fr.FR_ERR_DEVICE and "c001" in str(e.value)
+    assert torch.equal(got, want) and fr.fr_ops_sync_status(stream()) == 0

@@ -151,3 +151,11 @@ def test_declared_extents_need_the_checked_build(abi):
         with pytest.raises(abi.FrError) as e:
             abi.fr_debug_limit_op_extent(name, 10)
         assert e.value.code == code
+
+
+@pytest.mark.parametrize("sizes", [(1, 8, 1, 4, 1000, 128), (1, 8, 1, 1, 513, 64), (4, 16, 2, 24, 2148, 256)])
+def test_attention_scratch_too_small_is_refused(abi, sizes):
+    lib, n = abi.load_library(), abi.fr_attention_tree_scratch_bytes(*sizes)
+    assert n > 0
+    for scratch, size in ((None, n), (A, n - 1), (A, 0)):
+        assert lib.fr_attention_tree(A, A, A, A, A, A, A, *sizes, scratch, size, None) == abi.FR_ERR_SHAPE, abi.fr_last_error()
