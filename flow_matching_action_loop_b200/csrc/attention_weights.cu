@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(AW_THREADS, 1) k_attn_weights(const __grid_con
             const int tok = (r0 + tid) % a.N;
             const bool counts = !a.use || ((a.use[static_cast<size_t>(it.b) * a.W + (tok >> 5)] >> (tok & 31)) & 1u);
             const float v = lse[r0 + tid];
+            // (one float32 rounding of the exponent: no more than half a step of lse itself gives the weight)
             if (counts && v != -INFINITY) x = -v * 1.4426950408889634f;
           }
           lse_sh[tid] = x;

@@ -505,7 +505,11 @@ int fr_attention_noalloc(const void* q, const void* k, const void* v, void* o, i
  * program that decodes drafted tokens is: write the drafts' K/V, fr_attention_tree per layer, decide
  * what to accept, fr_attention_weights (when the cache is to be trimmed), fr_cache_commit, and now and
  * then fr_cache_evict.  No counterpart in the pages: they serve a policy that decodes discrete tokens
- * (a subtask, action tokens) on the backbone's cache after fr_prefill, and histories that outgrow it.
+ * (a subtask, action tokens) on the backbone's cache after fr_prefill, and histories that outgrow it.  The program
+ * brings the drafts' q, K and V (K rotated at the token's position), and it alone knows the lengths and, after
+ * fr_cache_evict, the positions: fr_denoise reads a prefix of one length per call, as fr_set_prefix_kv, fr_prefill or
+ * fr_capsule_restore left it, and puts the action tokens at positions P on.  A cache that these ops have grown or
+ * trimmed is for the program's own decoder.
  *
  * Common to the four:
  *   - lens is device int32 [B], so a captured graph follows the sequences' growth.  lens[b] < 0 marks a
@@ -550,9 +554,11 @@ int fr_tree_mask(const int32_t* parents, int n, uint32_t* mask);
  * words as fr_tree_mask writes them, any bits (a token need not see itself), or NULL: a sequence, token i
  * sees drafted tokens 0..i (N = 1 is the decoding of single tokens).  o: bf16 [B][N][Hq*dh] (the layout of
  * fr_attention); lse: float32 [B][Hq][N], or NULL.  A row that sees no key has o = 0 and lse = -inf.
- * What a token does not see cannot reach its row, whatever it holds; a drafted value row that holds a NaN
- * or an infinity makes the whole o row of the tokens that see it NaN.  A NaN among the scores that a row
- * sees makes its o and lse NaN.
+ * What a token does not see cannot reach its row, whatever it holds.  A drafted value row that holds a NaN
+ * or an infinity makes the whole o row of the tokens that see it NaN; a committed one, which all tokens see, makes
+ * the features that hold them NaN or infinite.  A NaN or +infinity among the scores that a row sees makes its o
+ * and lse NaN.  Scores, sums and o are float32; the weights of a tile are rounded to bf16, the tensor core's operand
+ * type, before they meet the values (as in fr_attention), and o once more when it is written.
  * scratch: fr_attention_tree_scratch_bytes() bytes (NULL when that is 0; 40 MiB cover every size).
  * Limits: dh in {64, 128, 256}, Hq % Hkv == 0, N <= FR_TREE_MAX_NODES, S_max <= FR_CACHE_MAX_SLOTS,
  * B <= 4096, Hq <= 1024, and B * Hkv * ceil(Hq / Hkv * N / 128) * ceil(S_max / 128) < 2^31.
@@ -570,7 +576,8 @@ size_t fr_attention_tree_scratch_bytes(int B, int Hq, int Hkv, int N, int S_max,
  * the rows that see slot s.  acc float32 [B][Hkv][S_max]: committed slots acc[s] += w[s], drafted slots
  * acc[s] = w[s]; later slots stay as they were.  q, k, lens, mask as fr_attention_tree had them, lse as it
  * left them (a row of lse = -inf gives nothing); use: [B][ceil(N/32)] words, bit i set when token i
- * counts (say, was accepted), or NULL: all.  Rows that give nothing may hold anything in q.
+ * counts (say, was accepted), or NULL: all.  Rows that give nothing may hold anything in q.  w is summed over all
+ * rows in float32 and added once.
  * Limits: those of fr_attention_tree.
  */
 int fr_attention_weights(const void* q, const void* k, const float* lse, const int32_t* lens, const uint32_t* mask,

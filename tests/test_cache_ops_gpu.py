@@ -972,3 +972,31 @@ def test_attention_weights_refuse_bad_lengths_on_the_device(spec):
         fr.fr_ops_sync_status(stream())
     assert e.value.code == fr.FR_ERR_DEVICE and "c001" in str(e.value)
     assert torch.equal(got, want) and fr.fr_ops_sync_status(stream()) == 0
+
+
+# a cluster per unit, units whole, units cut between CTAs
+@pytest.mark.parametrize("spec", [(2, 8, 1, 256, 7, 3000, [2900, 2500]), (40, 8, 8, 64, 2, 200, [150 + b % 40 for b in range(40)]),
+                                  (24, 16, 8, 128, 3, 4200, [4190 - 97 * b for b in range(24)])], ids=lambda s: "-".join(map(str, s[:6])))
+def test_committed_rows_that_are_not_finite(spec):
+    """Values reach the features that hold them, of the rows of their KV head; a NaN or infinite score, its whole row."""
+    c = Case(*spec, "tree").device()
+    c.run()
+    o, lse = c.o.clone().view(c.B, c.N, c.Hq, c.dh), c.lse.clone()
+    g, b, h = c.Hq // c.Hkv, c.B - 1, c.Hkv - 1
+    rows = slice(h * g, (h + 1) * g)
+    c.dv[b, h, c.lens[b] // 2, 5], c.dv[b, h, 0, 33], c.dv[b, h, c.lens[b] - 1, 60] = float("nan"), float("inf"), float("-inf")
+    c.run()
+    o2 = c.o.clone().view(o.shape)
+    assert not torch.isfinite(o2[b, :, rows][..., [5, 33, 60]]).any()
+    for f in (5, 33, 60):
+        o2[b, :, rows, f] = o[b, :, rows, f]
+    assert torch.equal(o2, o) and torch.equal(c.lse, lse)
+    c.dv.copy_(c.v)
+    c.dk[b, h, c.lens[b] // 3, 2] = float("nan")
+    c.run()
+    o2 = c.o.clone().view(o.shape)
+    assert torch.isnan(o2[b, :, rows]).all() and torch.isnan(c.lse[b, rows]).all()
+    o2[b, :, rows] = o[b, :, rows]
+    c.lse[b, rows] = lse[b, rows]
+    assert torch.equal(o2, o) and torch.equal(c.lse, lse)
+    assert fr.fr_ops_sync_status(stream()) == 0
