@@ -1000,3 +1000,36 @@ def test_committed_rows_that_are_not_finite(spec):
     c.lse[b, rows] = lse[b, rows]
     assert torch.equal(o2, o) and torch.equal(c.lse, lse)
     assert fr.fr_ops_sync_status(stream()) == 0
+
+
+def test_weights_of_many_rows_in_a_graph_and_on_two_streams():
+    """Several passes of rows: a captured call follows the lengths; two calls that overlap in time do not share anything."""
+    a, b = Case(3, 8, 1, 128, 90, 5000, [4900, 17, 4000], "tree").device(), Case(3, 8, 1, 128, 90, 5000, [1000, 4910, -1], "tree", seed=4).device()
+    a.run(), b.run()
+    acc0 = torch.rand(3, 1, 5000).cuda() * 100
+
+    def weights(c, acc):
+        fr.fr_attention_weights(ptr(c.dq), ptr(c.dk), ptr(c.lse), ptr(c.dlens), ptr(c.dwords), 0, ptr(acc), 3, 8, 1, 90, 5000, 128,
+                                torch.cuda.current_stream().cuda_stream)
+
+    want = [acc0.clone(), acc0.clone()]
+    weights(a, want[0]), weights(b, want[1])
+    assert not torch.equal(*want)
+    got, s = [acc0.clone(), acc0.clone()], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for c, x, st in zip((a, b), got, s):
+        with torch.cuda.stream(st):
+            for _ in range(4):
+                x.copy_(acc0)
+                weights(c, x)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    acc, graph = acc0.clone(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s[0]):
+        weights(a, acc)
+    graph.replay()
+    assert torch.equal(acc, want[0])
+    for x, y in ((a.dq, b.dq), (a.dk, b.dk), (a.lse, b.lse), (a.dlens, b.dlens), (a.dwords, b.dwords), (acc, acc0)):
+        x.copy_(y)
+    graph.replay()
+    assert torch.equal(acc, want[1]) and fr.fr_ops_sync_status(stream()) == 0
