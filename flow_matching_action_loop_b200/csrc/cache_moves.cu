@@ -82,11 +82,14 @@ __global__ void __launch_bounds__(CM_THREADS) k_cache_commit(const __grid_consta
 // have the same number over the cluster.  The r-th hole takes the r-th mover: only those rows of K and V
 // move, and as no hole is a mover the copies need no order.
 //
-// At 16 samples of up to 16384 slots, 8 heads of 128 bf16 features, trimmed to 12001: 80 us, of it 25 us selection
-// and 45 us moves of 256-byte rows (119 MB written, as many read, 5.3 TB/s), which the memory bounds.
+// At 16 samples of up to 16384 slots, 8 heads of 128 bf16 features, trimmed to 12001: 81 us.  Keys are made after 13.5
+// us, digits found after 21.5, lists joined after 26; the median CTA has moved its rows after 68 (119 MB written, as
+// many read, 5.3 TB/s) and those of the longest samples after 82: HBM idles during the selection and partly at the end.
 // Two CTAs of 512 threads per KV head and sample there; four took 87 us, four of 256 threads 84 us, two of 1024
-// 100 us, one 133 us.  One head of 866 slots trimmed to 512: 10.2 us, a chain of cluster barriers (1 us each
-// with the reads behind it).
+// 100 us, one 133 us.  One head of 866 slots trimmed to 512: 10.4 us, of it 1.2 keys, 3.3 digits and 1.8 lists (a
+// cluster barrier of 1 us each with the reads behind it), 2.4 moves, 0.6 the last barrier: what four CTAs cost each other;
+// one CTA with all keys would need none.  float32 rows of 128 features, 8 x 8192 slots of 4 heads to 6001: 29 us for
+// 12.6 at the rate of a copy.
 constexpr int EV_THREADS = 512, EV_WARPS = EV_THREADS / 32;
 constexpr int EV_MAX_CLUSTER = 16;
 constexpr int EV_SLICE_BYTES = 6;   // per slot of a slice: key (4) + list entry (2)

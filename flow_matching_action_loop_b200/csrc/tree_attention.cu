@@ -30,7 +30,8 @@
 // One group's loads, maxima and stores thus overlap the other's exponentials (with both groups on one tile,
 // half a row each, the multi-function unit idled more than half of a tile's 2500 cycles).  The groups hand the row's
 // reference on from tile to tile.  Two score buffers (LA = 2) let both groups have a tile; at dh = 256
-// tensor memory has room for one (LA = 1), and S(t+1) is issued once the scores of tile t are in registers.
+// tensor memory has room for one of 128 slots (LA = 1), and S(t+1) is issued once the scores of tile t are in
+// registers.  (Buffers of 64 slots would leave room for two; not tried.)
 // P has columns of its own: with P in those of the scores, S(t+1) waited for P(t-1) V(t-1) as well (1.97 us a
 // tile at dh = 256 instead of 1.6).
 // The reference of a row's exponentials moves only when its maximum has grown by more than 2^8 (P stays
@@ -38,10 +39,18 @@
 // P is rounded to bf16, the tensor core's operand type: half a bf16 step per weight, as much as the
 // rounding of o itself.
 //
-// Single tokens of 32 samples with up to 8191 slots, 8 KV heads of 128: 112 us, 665 MB at 5.9 TB/s (memory).  Trees of
-// 63 tokens over 6 x 32767 slots, 8 query heads of 256: 99 us, 990 TFLOP/s, the tensor pipe 64 % active (one score
-// buffer).  One token over 816 slots: 9.5 us, of it 1 us set-up, 1.5 to the first scores, 2 a tile, 1.5 to O in shared
-// memory, 2 the join.
+// Single tokens of 32 samples with up to 8191 slots, 8 KV heads of 128: 113 us, 665 MB at 5.9 TB/s (memory); CTAs end
+// between 97 and 108 us.  Trees of 63 tokens over 6 x 32767 slots, 8 query heads of 256: 104 us, 940 TFLOP/s, the
+// tensor pipe 62 % active (one score buffer); CTAs end between 81 and 91 us, the merge follows.
+// Short cases, us from the launch (median CTA; the last one in brackets):
+//                                                  set-up  scores  tiles       O    all rows  weights  joined
+//   one token over 816 slots, 8/1 heads of 256        1.0    2.3    3.8 (4.7)  5.2    6.5       7.5     8.3, of 9.8
+//   4 trees of 24 over 2048, 16/2 heads of 128        1.0    2.2    5.5 (7.1)  6 (8)  8.0 (8.6) 9.2    10.7 (12.5), of 13.8
+//   2 x 128 tokens over 4095, 16/16 heads of 64       1.2    2.0   10.6 (14.3) 12 (15) 15 (16)  16     17.6 (18.7), of 22
+// so a CTA that runs few tiles of 128 rows takes about 1.3 us for each (S, softmax and P V of one row tile one after
+// the other), and the join 4 us: the cluster's barrier, then two trips to the other CTAs' memory.
+// k_tree_attn spills: 152 to 160 bytes of stores and 288 to 296 of loads in its shared-line form, 52 and 40 with a
+// cluster, none in the merge.
 #include <algorithm>
 #include <cooperative_groups.h>
 #include <type_traits>
@@ -62,7 +71,7 @@ constexpr int TA_THREADS = TA_SOFTMAX + 128;   // + a warpgroup of the copy warp
 // fewer registers, the growing warpgroups would wait for good.  tree_init refuses such a build.)
 constexpr int TA_REGS = 168, TA_REGS_SOFTMAX = 208, TA_REGS_OTHER = 88;
 static_assert(2 * TA_REGS_SOFTMAX + TA_REGS_OTHER == 3 * TA_REGS, "registers are only moved");
-constexpr int TA_CTAS = 148;                   // at most: the scratch holds two segments' rows for each
+constexpr int TA_CTAS = 148;                   // at most (the SMs of a B200): the scratch holds two segments' rows for each
 constexpr float TA_RESCALE = 8.f;
 constexpr int TA_CLUSTER = 16;                 // CTAs of a cluster at most
 
@@ -900,7 +909,7 @@ cudaError_t tree_init(int* clusters, int* regs) {
 
 // CTAs of a unit's cluster, or 1: tiles shared over the whole GPU.  A cluster is taken if all of them are
 // resident together and a CTA's tiles, with every sample as long as the cache, are at most CLUSTER_EXTRA above an
-// equal share of all tiles over the GPU: a tile takes about 0.6 us there, the merge kernel and a CTA's second
+// equal share of all tiles over the GPU: a tile takes 0.6 to 1.3 us there, the merge kernel and a CTA's second
 // segment 4 us and more.  The lengths are not known here: of one long sample among short ones a cluster's CTAs run
 // the same tiles, and the others idle.  So a CTA has at most CLUSTER_TILES.  Single tokens, 72 units of 256
 // features, us for clusters / shared tiles: 33 tiles (17 a CTA) 54 / 62 with all samples long, 36 / 26 with one, 44 /
